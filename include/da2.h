@@ -270,6 +270,70 @@ int da2_last_cuda_error(void);
 /* Static string naming a status. */
 const char* da2_status_string(da2_status status);
 
+/* ------------------------------------------------------------------------------------
+ * Operators around the self-attention of a video-DiT block: the norm and position rotation
+ * of its queries and keys in front of da2_prepare, with its backward pass. No counterpart in
+ * the papers.
+ *
+ * Their tensors are given by a base pointer and element strides of batch, head and token
+ * (channels are contiguous), so [B,H,T,d], [B,T,H,d] and slices of a fused projection all go
+ * in as they are. Base pointers must be 16-byte aligned and strides multiples of 8 elements
+ * (DA2_ERR_ALIGNMENT otherwise); the stride of an axis longer than one must be positive
+ * (DA2_ERR_INVALID_ARG otherwise: a zero or negative stride would let rows overlap); the
+ * stride of an axis of length one is not read. Outputs must not overlap each other or, but
+ * where a call says otherwise, an input. d is 64 or 128 and the element type bf16 or fp16.
+ * Every sum, norm and softmax statistic is fp32; each output is rounded once.
+ * The calls are asynchronous on `stream`, allocate nothing, keep nothing between calls and
+ * can be captured into a CUDA graph; two calls that may overlap need workspaces of their own. */
+typedef struct da2_tensor {
+  void* data;           /* element (0, 0, 0, 0) */
+  int64_t sb, sh, st;   /* element strides of batch, head and token */
+} da2_tensor;
+
+enum { DA2_DTYPE_BF16 = 0, DA2_DTYPE_F16 = 1 };
+
+enum {
+  /* rotate the channel pairs (c, c + d/2) instead of (2c, 2c + 1) */
+  DA2_ROPE_HALVES = 1,
+  /* the tables are [B][T_rot][d/2] instead of [T_rot][d/2] shared by the batch */
+  DA2_ROPE_BATCHED = 2
+};
+
+/* One call of the norm and rotation. */
+typedef struct da2_norm_rope_config {
+  int B, Hq, Hk, T, d;  /* batch, query heads, key heads (0: no keys), tokens, head dim */
+  int T_rot;            /* tokens 0 .. T_rot-1 are rotated (0: the norm alone) */
+  float eps;            /* added to the mean square; finite, >= 0 */
+  int dtype;            /* DA2_DTYPE_* of q, k and their outputs and gradients */
+  int flags;            /* DA2_ROPE_* bits */
+} da2_norm_rope_config;
+
+/* RMS norm of each head of q and k and the position rotation, in one pass:
+     n = x / sqrt(mean_c(x_c^2) + eps),  y = n * w,
+     (y_a, y_b) -> (y_a cos - y_b sin, y_a sin + y_b cos) for channel pair i = (a, b)
+   with cos, sin = row t (the token) and column i of the tables. wq, wk: fp32 [d], shared by
+   the heads; NULL means all ones. cos_t, sin_t: fp32, 16-byte aligned; not read when T_rot is
+   0. q_out may be q and k_out may be k (the same pointer and strides). k and k_out are not
+   read when Hk is 0 and may be NULL. */
+da2_status da2_qk_norm_rope(const da2_norm_rope_config* cfg, const da2_tensor* q, const da2_tensor* k,
+                            const float* wq, const float* wk, const float* cos_t, const float* sin_t,
+                            const da2_tensor* q_out, const da2_tensor* k_out, cudaStream_t stream);
+
+/* Workspace bytes of da2_qk_norm_rope_backward (host only, no CUDA call). */
+da2_status da2_qk_norm_rope_workspace_size(const da2_norm_rope_config* cfg, size_t* bytes);
+
+/* Gradients of da2_qk_norm_rope: dq_out, dk_out are the gradients of its outputs, q, k its
+   inputs. With g = the gradient rotated back,
+     dw = sum over rows of g * n,  dx = (g w - n mean_c(g w n)) / sqrt(mean_c(x^2) + eps).
+   dq may be dq_out or q, dk may be dk_out or k. dwq, dwk: fp32 [d], overwritten; NULL skips
+   them. The sums run in a fixed order: equal inputs give equal bits. ws: 256-byte aligned. */
+da2_status da2_qk_norm_rope_backward(const da2_norm_rope_config* cfg, const da2_tensor* dq_out,
+                                     const da2_tensor* dk_out, const da2_tensor* q, const da2_tensor* k,
+                                     const float* wq, const float* wk, const float* cos_t,
+                                     const float* sin_t, const da2_tensor* dq, const da2_tensor* dk,
+                                     float* dwq, float* dwk, void* ws, size_t ws_bytes,
+                                     cudaStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -101,6 +101,7 @@ def lib():
             "da2_get_error": [vp, sz, cp, vp, ctypes.POINTER(ctypes.c_uint32)],
             "da2_forward_noalloc": [cp, vp, vp, vp, vp, vp],
             "da2_check_selection": [cp, vp, sz, vp],
+            **SIGNATURES,
         }
         for name, args in sigs.items():
             fn = getattr(L, name)
@@ -118,7 +119,8 @@ def lib():
 EXPORTED = ("da2_workspace_size", "da2_workspace_views", "da2_prepare", "da2_draft_select",
             "da2_attention", "da2_forward", "da2_forward_host", "da2_get_error",
             "da2_status_string", "da2_forward_noalloc", "da2_last_cuda_error",
-            "da2_check_selection")
+            "da2_check_selection", "da2_qk_norm_rope", "da2_qk_norm_rope_workspace_size",
+            "da2_qk_norm_rope_backward")
 
 
 def config(w, flags: int = 0, sm_scale: float = 0.0) -> Config:
@@ -271,3 +273,9 @@ def get_error(cfg, ws, stream=None) -> int:
     if st not in (0, 6):
         raise DA2Error("da2_get_error", st)
     return word.value
+
+
+# the operators of the block around the attention (they use the helpers above)
+from .block_ops import (  # noqa: E402
+    ROPE_BATCHED, ROPE_HALVES, SIGNATURES, NormRopeConfig, norm_rope_config, qk_norm_rope,
+    qk_norm_rope_workspace_size, qk_norm_rope_workspace, qk_norm_rope_backward)

@@ -1,0 +1,194 @@
+"""Operators of a video-DiT block around the sparse self-attention: the RMS norm and position
+rotation of its queries and keys, with its backward pass (see include/da2.h). Argument marshalling only, like the package's other
+calls; the names are re-exported by the package.
+
+    cfg = norm_rope_config(B, Hq, Hk, T, d, layout="bthd")
+    qk_norm_rope(cfg, q, k, wq, wk, cos, sin, q_out, k_out)          # then da2.forward(...)
+
+Activations are [B, H, T, d] (layout "bhtd") or [B, T, H, d] ("bthd"), bf16 or fp16, with
+contiguous channels; the other strides are free (a slice of a fused projection goes in as it
+is), multiples of 8 elements. A call runs on the given stream's device, whichever device is
+current.
+"""
+from __future__ import annotations
+
+import contextlib
+import ctypes
+
+import sparse_mixed_precision_b200 as _pkg
+
+ROPE_HALVES = 1
+ROPE_BATCHED = 2
+
+
+class Tensor(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("sb", ctypes.c_int64), ("sh", ctypes.c_int64), ("st", ctypes.c_int64)]
+
+
+class NormRopeConfig(ctypes.Structure):
+    """da2_norm_rope_config; `layout` is kept for the binding's shape checks."""
+    _fields_ = [(n, ctypes.c_int) for n in ("B", "Hq", "Hk", "T", "d", "T_rot")] + \
+               [("eps", ctypes.c_float), ("dtype", ctypes.c_int), ("flags", ctypes.c_int)]
+    layout = "bhtd"
+
+
+_vp, _sz, _tp = ctypes.c_void_p, ctypes.c_size_t, ctypes.POINTER(Tensor)
+_np, _szp = ctypes.POINTER(NormRopeConfig), ctypes.POINTER(ctypes.c_size_t)
+SIGNATURES = {
+    "da2_qk_norm_rope": [_np, _tp, _tp, _vp, _vp, _vp, _vp, _tp, _tp, _vp],
+    "da2_qk_norm_rope_workspace_size": [_np, _szp],
+    "da2_qk_norm_rope_backward": [_np, _tp, _tp, _tp, _tp, _vp, _vp, _vp, _vp, _tp, _tp, _vp, _vp, _vp, _sz, _vp],
+}
+
+
+def _dtypes():
+    import torch
+    return {torch.bfloat16: 0, torch.float16: 1}
+
+
+def _dtype_code(dtype):
+    import torch
+    dtype = torch.bfloat16 if dtype is None else dtype
+    if dtype not in _dtypes():
+        raise ValueError(f"dtype must be bfloat16 or float16, not {dtype}")
+    return _dtypes()[dtype]
+
+
+def _with_layout(cfg, layout):
+    if layout not in ("bhtd", "bthd"):
+        raise ValueError(f"layout must be 'bhtd' or 'bthd', not {layout!r}")
+    cfg.layout = layout
+    return cfg
+
+
+def norm_rope_config(B, Hq, Hk, T, d, dtype=None, T_rot=None, eps=1e-6, layout="bhtd", half=False,
+                     batched=False) -> NormRopeConfig:
+    """da2_norm_rope_config. dtype: bfloat16 (the default) or float16; T_rot: rotated tokens
+    (all of them by default); half: rotate channel pairs (c, c + d/2) instead of (2c, 2c + 1);
+    batched: tables [B, T_rot, d/2] instead of [T_rot, d/2]. Hk = 0: queries only."""
+    flags = (ROPE_HALVES if half else 0) | (ROPE_BATCHED if batched else 0)
+    return _with_layout(NormRopeConfig(B, Hq, Hk, T, d, T if T_rot is None else T_rot, float(eps),
+                                       _dtype_code(dtype), flags), layout)
+
+
+class _Args:
+    """Checks a call's tensors (the C ABI sees bare pointers) and turns them into its arguments.
+    Every device tensor must sit on the device of the stream the call runs on."""
+
+    def __init__(self, fn, cfg, stream):
+        import torch
+        self.fn, self.cfg, self.torch, self._given = fn, cfg, torch, stream
+
+    @property
+    def stream(self):
+        if self._given is None:
+            self._given = self.torch.cuda.current_stream()
+        return self._given
+
+    def _device(self, name, t):
+        if not isinstance(t, self.torch.Tensor):
+            raise TypeError(f"{self.fn}: {name} must be a torch.Tensor")
+        if t.device.type != "cuda":
+            raise ValueError(f"{self.fn}: {name} must be a CUDA tensor, not on {t.device}")
+        if t.device != self.stream.device:
+            raise ValueError(f"{self.fn}: {name} is on {t.device} but the call runs on {self.stream.device}")
+
+    def act(self, name, t, H, T):
+        """A strided activation of H heads and T tokens."""
+        cfg = self.cfg
+        if not isinstance(t, self.torch.Tensor):
+            raise TypeError(f"{self.fn}: {name} must be a torch.Tensor")
+        if _dtypes().get(t.dtype) != cfg.dtype:
+            raise ValueError(f"{self.fn}: {name} has dtype {t.dtype}; the configuration needs "
+                             f"{[d for d, c in _dtypes().items() if c == cfg.dtype][0]}")
+        bthd = cfg.layout == "bthd"
+        want = (cfg.B, T, H, cfg.d) if bthd else (cfg.B, H, T, cfg.d)
+        if tuple(t.shape) != want:
+            raise ValueError(f"{self.fn}: {name} has shape {tuple(t.shape)}; the configuration needs {want}")
+        if t.stride(3) != 1:
+            raise ValueError(f"{self.fn}: {name} must have contiguous channels")
+        self._device(name, t)
+        sh, st = (t.stride(2), t.stride(1)) if bthd else (t.stride(1), t.stride(2))
+        return ctypes.byref(Tensor(t.data_ptr(), t.stride(0), sh, st))
+
+    def plain(self, name, t, dtype, shape):
+        """A contiguous tensor of one shape, or None."""
+        if t is None:
+            return None
+        if not isinstance(t, self.torch.Tensor):
+            raise TypeError(f"{self.fn}: {name} must be a torch.Tensor")
+        if t.dtype != dtype:
+            raise ValueError(f"{self.fn}: {name} must be {dtype}, not {t.dtype}")
+        if tuple(t.shape) != tuple(shape):
+            raise ValueError(f"{self.fn}: {name} has shape {tuple(t.shape)}; the call needs {tuple(shape)}")
+        if not t.is_contiguous():
+            raise ValueError(f"{self.fn}: {name} must be contiguous")
+        self._device(name, t)
+        return ctypes.c_void_p(t.data_ptr())
+
+    def buffer(self, name, t):
+        """A contiguous byte buffer: (pointer, size)."""
+        if not isinstance(t, self.torch.Tensor):
+            raise TypeError(f"{self.fn}: {name} must be a torch.Tensor")
+        if not t.is_contiguous():
+            raise ValueError(f"{self.fn}: {name} must be contiguous")
+        self._device(name, t)
+        return ctypes.c_void_p(t.data_ptr()), t.numel() * t.element_size()
+
+    def call(self, *args):
+        device = self.stream.device
+        here = self.torch.cuda.current_device() == device.index
+        with contextlib.nullcontext() if here else self.torch.cuda.device(device):
+            st = getattr(_pkg.lib(), self.fn)(ctypes.byref(self.cfg), *args, ctypes.c_void_p(self.stream.cuda_stream))
+        _pkg._check(self.fn, st)
+
+
+def _size(fn, cfg):
+    n = ctypes.c_size_t()
+    _pkg._check(fn, getattr(_pkg.lib(), fn)(ctypes.byref(cfg), ctypes.byref(n)))
+    return n.value
+
+
+def _norm_args(a, cfg, wq, wk, cos, sin):
+    f32 = a.torch.float32
+    table = (cfg.T_rot, cfg.d // 2) if not cfg.flags & ROPE_BATCHED else (cfg.B, cfg.T_rot, cfg.d // 2)
+    if cfg.T_rot > 0 and (cos is None or sin is None):
+        raise ValueError(f"{a.fn}: cos and sin are needed to rotate {cfg.T_rot} tokens")
+    if cfg.T_rot == 0:
+        cos = sin = None
+    return (a.plain("wq", wq, f32, (cfg.d,)), a.plain("wk", wk, f32, (cfg.d,)),
+            a.plain("cos", cos, f32, table), a.plain("sin", sin, f32, table))
+
+
+def _key_act(a, cfg, name, t):
+    return a.act(name, t, cfg.Hk, cfg.T) if cfg.Hk else None
+
+
+def qk_norm_rope(cfg, q, k, wq, wk, cos, sin, q_out, k_out, stream=None):
+    """RMS norm of every head of q and k and the position rotation. wq, wk: float32 [d] or None
+    (ones); cos, sin: float32 [T_rot, d/2] ([B, T_rot, d/2] with batched=True); q_out may be q and
+    k_out may be k. k and k_out are not used when Hk is 0."""
+    a = _Args("da2_qk_norm_rope", cfg, stream)
+    a.call(a.act("q", q, cfg.Hq, cfg.T), _key_act(a, cfg, "k", k), *_norm_args(a, cfg, wq, wk, cos, sin),
+           a.act("q_out", q_out, cfg.Hq, cfg.T), _key_act(a, cfg, "k_out", k_out))
+
+
+def qk_norm_rope_workspace_size(cfg) -> int:
+    return _size("da2_qk_norm_rope_workspace_size", cfg)
+
+
+def qk_norm_rope_workspace(cfg, device):
+    """A workspace for qk_norm_rope_backward."""
+    import torch
+    return torch.empty(qk_norm_rope_workspace_size(cfg), dtype=torch.uint8, device=device)
+
+
+def qk_norm_rope_backward(cfg, dq_out, dk_out, q, k, wq, wk, cos, sin, dq, dk, dwq, dwk, ws, stream=None):
+    """Gradients of qk_norm_rope: dq, dk (of q, k) and dwq, dwk (float32 [d], or None) from
+    dq_out, dk_out (of its outputs) and its inputs. dq may be dq_out or q, dk may be dk_out or k."""
+    a = _Args("da2_qk_norm_rope_backward", cfg, stream)
+    f32 = a.torch.float32
+    dw = a.plain("dwq", dwq, f32, (cfg.d,)), a.plain("dwk", dwk, f32, (cfg.d,))
+    a.call(a.act("dq_out", dq_out, cfg.Hq, cfg.T), _key_act(a, cfg, "dk_out", dk_out),
+           a.act("q", q, cfg.Hq, cfg.T), _key_act(a, cfg, "k", k), *_norm_args(a, cfg, wq, wk, cos, sin),
+           a.act("dq", dq, cfg.Hq, cfg.T), _key_act(a, cfg, "dk", dk), *dw, *a.buffer("ws", ws))

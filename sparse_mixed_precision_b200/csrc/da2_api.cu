@@ -2,8 +2,7 @@
 #include <cmath>
 #include <cstring>
 
-#include <nvtx3/nvToolsExt.h>
-
+#include "api.cuh"
 #include "checks.cuh"
 #include "common.cuh"
 #include "split_tiles.cuh"
@@ -25,10 +24,6 @@ constexpr int kMaxBlocks = 4096;
 constexpr long kMaxHeads = 65535;   // B * H: the stage kernels put the heads on the grid's y axis
 
 bool pct_ok(int p) { return p >= 0 && p <= 100; }
-
-size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
-
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 da2_status check_config(const da2_config* c) {
   if (!c) return DA2_ERR_INVALID_ARG;
@@ -191,19 +186,6 @@ da2_status setup(const da2_config* cfg, void* ws, size_t ws_bytes, da2_views* v,
 // cudaGetLastError has consumed it by the time the caller could ask the runtime).
 thread_local cudaError_t g_last_cuda = cudaSuccess;
 
-da2_status cuda_status(cudaError_t e) {
-  if (e == cudaSuccess) return DA2_OK;
-  g_last_cuda = e;
-  return DA2_ERR_CUDA;
-}
-
-// An NVTX range around one library call (visible in a profiler's timeline; no cost without
-// an attached tool).
-struct NvtxRange {
-  explicit NvtxRange(const char* name) { nvtxRangePushA(name); }
-  ~NvtxRange() { nvtxRangePop(); }
-};
-
 // End of a stage call: with DA2_FLAG_DEBUG_CANARY the guard regions are checked (a change
 // sets kErrCanary in the error word); a DA2_DEBUG build then waits for the stream and
 // returns DA2_ERR_TIMEOUT at once if the error word is set (the word stays set for
@@ -222,6 +204,14 @@ da2_status finish_stage(const da2_config* cfg, const Ws& w, void* ws, const Guar
 }
 
 }  // namespace
+
+namespace da2 {
+da2_status cuda_status(cudaError_t e) {
+  if (e == cudaSuccess) return DA2_OK;
+  g_last_cuda = e;
+  return DA2_ERR_CUDA;
+}
+}  // namespace da2
 
 extern "C" {
 
