@@ -272,8 +272,8 @@ const char* da2_status_string(da2_status status);
 
 /* ------------------------------------------------------------------------------------
  * Operators around the self-attention of a video-DiT block: the norm and position rotation
- * of its queries and keys in front of da2_prepare, with its backward pass. No counterpart in
- * the papers.
+ * of its queries and keys in front of da2_prepare, and the attention of its tokens to an
+ * encoder's states, each with its backward pass. No counterpart in the papers.
  *
  * Their tensors are given by a base pointer and element strides of batch, head and token
  * (channels are contiguous), so [B,H,T,d], [B,T,H,d] and slices of a fused projection all go
@@ -333,6 +333,37 @@ da2_status da2_qk_norm_rope_backward(const da2_norm_rope_config* cfg, const da2_
                                      const float* sin_t, const da2_tensor* dq, const da2_tensor* dk,
                                      float* dwq, float* dwk, void* ws, size_t ws_bytes,
                                      cudaStream_t stream);
+
+/* One call of the attention to an encoder's states. */
+typedef struct da2_cross_config {
+  int B, H, Hkv;        /* batch, query heads, key/value heads (Hkv divides H; query head h uses
+                           key/value head h / (H / Hkv)) */
+  int Tq, Tk, d;        /* queries, keys, head dim */
+  float sm_scale;       /* softmax scale; 0 selects 1/sqrt(d) */
+  int dtype;            /* DA2_DTYPE_* of every activation and gradient */
+  int flags;            /* 0, or DA2_FLAG_TEST_STALL */
+} da2_cross_config;
+
+/* Workspace bytes of da2_cross_attention (host only, no CUDA call). */
+da2_status da2_cross_attention_workspace_size(const da2_cross_config* cfg, size_t* bytes);
+
+/* Attention of Tq queries to Tk keys of another sequence:
+     s = q k^T sm_scale,  p = softmax over keys 0 .. len[b]-1,  out = p v,
+     lse = ln sum exp(s)  (fp32 [B][H][Tq]; NULL: not written).
+   kv_len: device int32 [B], each taken into 0 .. Tk; NULL: Tk for every batch entry. Keys and
+   values behind the length do not reach the result, whatever they hold. A batch entry of length
+   0 has out = 0 and lse = -inf. Few query rows are split over their keys, the parts joined in a
+   fixed order: equal inputs give equal bits.
+   ws: 256-byte aligned; its first 256 bytes are the error area, to be zeroed once after the
+   workspace is allocated. A bounded device wait that runs out sets a bit there
+   (da2_cross_attention_get_error); nothing else in ws outlives the call. */
+da2_status da2_cross_attention(const da2_cross_config* cfg, const da2_tensor* q, const da2_tensor* k,
+                               const da2_tensor* v, const da2_tensor* out, float* lse, const int32_t* kv_len,
+                               void* ws, size_t ws_bytes, cudaStream_t stream);
+
+/* Reads the error word of a cross-attention workspace into *word and clears it (synchronises
+   `stream`): DA2_ERR_TIMEOUT if it was non-zero. */
+da2_status da2_cross_attention_get_error(void* ws, size_t ws_bytes, cudaStream_t stream, uint32_t* word);
 
 #ifdef __cplusplus
 }

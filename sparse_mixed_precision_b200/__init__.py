@@ -120,7 +120,8 @@ EXPORTED = ("da2_workspace_size", "da2_workspace_views", "da2_prepare", "da2_dra
             "da2_attention", "da2_forward", "da2_forward_host", "da2_get_error",
             "da2_status_string", "da2_forward_noalloc", "da2_last_cuda_error",
             "da2_check_selection", "da2_qk_norm_rope", "da2_qk_norm_rope_workspace_size",
-            "da2_qk_norm_rope_backward")
+            "da2_qk_norm_rope_backward", "da2_cross_attention_workspace_size", "da2_cross_attention",
+            "da2_cross_attention_get_error")
 
 
 def config(w, flags: int = 0, sm_scale: float = 0.0) -> Config:
@@ -277,5 +278,7 @@ def get_error(cfg, ws, stream=None) -> int:
 
 # the operators of the block around the attention (they use the helpers above)
 from .block_ops import (  # noqa: E402
-    ROPE_BATCHED, ROPE_HALVES, SIGNATURES, NormRopeConfig, norm_rope_config, qk_norm_rope,
-    qk_norm_rope_workspace_size, qk_norm_rope_workspace, qk_norm_rope_backward)
+    ROPE_BATCHED, ROPE_HALVES, SIGNATURES, NormRopeConfig, CrossConfig, norm_rope_config, cross_config, qk_norm_rope,
+    qk_norm_rope_workspace_size, qk_norm_rope_workspace, qk_norm_rope_backward,
+    cross_attention_workspace_size, cross_attention_workspace, cross_attention,
+    cross_attention_backward, cross_attention_get_error)

@@ -1,9 +1,15 @@
 """Operators of a video-DiT block around the sparse self-attention: the RMS norm and position
-rotation of its queries and keys, with its backward pass (see include/da2.h). Argument marshalling only, like the package's other
+rotation of its queries and keys, and the attention of its tokens to an encoder's states, each
+with its backward pass (see include/da2.h). Argument marshalling only, like the package's other
 calls; the names are re-exported by the package.
 
     cfg = norm_rope_config(B, Hq, Hk, T, d, layout="bthd")
     qk_norm_rope(cfg, q, k, wq, wk, cos, sin, q_out, k_out)          # then da2.forward(...)
+
+    cfg = cross_config(B, H, Tq, Tk, d)
+    ws = cross_attention_workspace(cfg, device)
+    cross_attention(cfg, q, k, v, out, ws, kv_len=lens, lse=lse)
+    cross_attention_backward(cfg, dout, q, k, v, out, lse, dq, dk, dv, ws_back, kv_len=lens)
 
 Activations are [B, H, T, d] (layout "bhtd") or [B, T, H, d] ("bthd"), bf16 or fp16, with
 contiguous channels; the other strides are free (a slice of a fused projection goes in as it
@@ -32,12 +38,22 @@ class NormRopeConfig(ctypes.Structure):
     layout = "bhtd"
 
 
+class CrossConfig(ctypes.Structure):
+    """da2_cross_config; `layout` is kept for the binding's shape checks."""
+    _fields_ = [(n, ctypes.c_int) for n in ("B", "H", "Hkv", "Tq", "Tk", "d")] + \
+               [("sm_scale", ctypes.c_float), ("dtype", ctypes.c_int), ("flags", ctypes.c_int)]
+    layout = "bhtd"
+
+
 _vp, _sz, _tp = ctypes.c_void_p, ctypes.c_size_t, ctypes.POINTER(Tensor)
-_np, _szp = ctypes.POINTER(NormRopeConfig), ctypes.POINTER(ctypes.c_size_t)
+_np, _xp, _szp = ctypes.POINTER(NormRopeConfig), ctypes.POINTER(CrossConfig), ctypes.POINTER(ctypes.c_size_t)
 SIGNATURES = {
     "da2_qk_norm_rope": [_np, _tp, _tp, _vp, _vp, _vp, _vp, _tp, _tp, _vp],
     "da2_qk_norm_rope_workspace_size": [_np, _szp],
     "da2_qk_norm_rope_backward": [_np, _tp, _tp, _tp, _tp, _vp, _vp, _vp, _vp, _tp, _tp, _vp, _vp, _vp, _sz, _vp],
+    "da2_cross_attention_workspace_size": [_xp, _szp],
+    "da2_cross_attention": [_xp, _tp, _tp, _tp, _tp, _vp, _vp, _vp, _sz, _vp],
+    "da2_cross_attention_get_error": [_vp, _sz, _vp, ctypes.POINTER(ctypes.c_uint32)],
 }
 
 
@@ -69,6 +85,13 @@ def norm_rope_config(B, Hq, Hk, T, d, dtype=None, T_rot=None, eps=1e-6, layout="
     flags = (ROPE_HALVES if half else 0) | (ROPE_BATCHED if batched else 0)
     return _with_layout(NormRopeConfig(B, Hq, Hk, T, d, T if T_rot is None else T_rot, float(eps),
                                        _dtype_code(dtype), flags), layout)
+
+
+def cross_config(B, H, Tq, Tk, d, Hkv=None, dtype=None, sm_scale=0.0, layout="bhtd", flags=0) -> CrossConfig:
+    """da2_cross_config. Hkv: key/value heads (H by default; must divide H); sm_scale: 0 selects
+    1/sqrt(d); dtype: bfloat16 (the default) or float16."""
+    return _with_layout(CrossConfig(B, H, H if Hkv is None else Hkv, Tq, Tk, d, float(sm_scale),
+                                    _dtype_code(dtype), int(flags)), layout)
 
 
 class _Args:
@@ -192,3 +215,54 @@ def qk_norm_rope_backward(cfg, dq_out, dk_out, q, k, wq, wk, cos, sin, dq, dk, d
     a.call(a.act("dq_out", dq_out, cfg.Hq, cfg.T), _key_act(a, cfg, "dk_out", dk_out),
            a.act("q", q, cfg.Hq, cfg.T), _key_act(a, cfg, "k", k), *_norm_args(a, cfg, wq, wk, cos, sin),
            a.act("dq", dq, cfg.Hq, cfg.T), _key_act(a, cfg, "dk", dk), *dw, *a.buffer("ws", ws))
+
+
+def cross_attention_workspace_size(cfg, backward=False) -> int:
+    return _size("da2_cross_attention_backward_workspace_size" if backward else
+                 "da2_cross_attention_workspace_size", cfg)
+
+
+def cross_attention_workspace(cfg, device, backward=False):
+    """A workspace for cross_attention (or its backward pass): its error word starts at zero."""
+    import torch
+    ws = torch.empty(cross_attention_workspace_size(cfg, backward), dtype=torch.uint8, device=device)
+    ws[:256].zero_()
+    return ws
+
+
+def _cross_args(a, cfg, lse, kv_len):
+    return (a.plain("lse", lse, a.torch.float32, (cfg.B, cfg.H, cfg.Tq)),
+            a.plain("kv_len", kv_len, a.torch.int32, (cfg.B,)))
+
+
+def cross_attention(cfg, q, k, v, out, ws, kv_len=None, lse=None, stream=None):
+    """out = softmax(q k^T sm_scale) v over each batch entry's first kv_len[b] keys (int32 [B];
+    None: all Tk). lse: float32 [B, H, Tq], or None when no backward pass follows."""
+    a = _Args("da2_cross_attention", cfg, stream)
+    a.call(a.act("q", q, cfg.H, cfg.Tq), a.act("k", k, cfg.Hkv, cfg.Tk), a.act("v", v, cfg.Hkv, cfg.Tk),
+           a.act("out", out, cfg.H, cfg.Tq), *_cross_args(a, cfg, lse, kv_len), *a.buffer("ws", ws))
+
+
+def cross_attention_backward(cfg, dout, q, k, v, out, lse, dq, dk, dv, ws, kv_len=None, stream=None):
+    """Gradients dq, dk, dv of cross_attention from dout, its inputs, its output and its lse. Keys
+    and values behind kv_len[b] get zero."""
+    a = _Args("da2_cross_attention_backward", cfg, stream)
+    if lse is None:
+        raise ValueError("da2_cross_attention_backward: lse is needed")
+    a.call(a.act("dout", dout, cfg.H, cfg.Tq), a.act("q", q, cfg.H, cfg.Tq), a.act("k", k, cfg.Hkv, cfg.Tk),
+           a.act("v", v, cfg.Hkv, cfg.Tk), a.act("out", out, cfg.H, cfg.Tq), *_cross_args(a, cfg, lse, kv_len),
+           a.act("dq", dq, cfg.H, cfg.Tq), a.act("dk", dk, cfg.Hkv, cfg.Tk), a.act("dv", dv, cfg.Hkv, cfg.Tk),
+           *a.buffer("ws", ws))
+
+
+def cross_attention_get_error(ws, stream=None) -> int:
+    """Reads and clears the error word of a cross_attention workspace (synchronises the stream)."""
+    import torch
+    s = torch.cuda.current_stream() if stream is None else stream
+    word = ctypes.c_uint32()
+    with torch.cuda.device(s.device):
+        st = _pkg.lib().da2_cross_attention_get_error(ctypes.c_void_p(ws.data_ptr()), ws.numel() * ws.element_size(),
+                                                      ctypes.c_void_p(s.cuda_stream), ctypes.byref(word))
+    if st not in (0, 6):
+        raise _pkg.DA2Error("da2_cross_attention_get_error", st)
+    return word.value
