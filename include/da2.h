@@ -344,8 +344,9 @@ typedef struct da2_cross_config {
   int flags;            /* 0, or DA2_FLAG_TEST_STALL */
 } da2_cross_config;
 
-/* Workspace bytes of da2_cross_attention (host only, no CUDA call). */
+/* Workspace bytes of da2_cross_attention and of its backward pass (host only, no CUDA call). */
 da2_status da2_cross_attention_workspace_size(const da2_cross_config* cfg, size_t* bytes);
+da2_status da2_cross_attention_backward_workspace_size(const da2_cross_config* cfg, size_t* bytes);
 
 /* Attention of Tq queries to Tk keys of another sequence:
      s = q k^T sm_scale,  p = softmax over keys 0 .. len[b]-1,  out = p v,
@@ -360,6 +361,18 @@ da2_status da2_cross_attention_workspace_size(const da2_cross_config* cfg, size_
 da2_status da2_cross_attention(const da2_cross_config* cfg, const da2_tensor* q, const da2_tensor* k,
                                const da2_tensor* v, const da2_tensor* out, float* lse, const int32_t* kv_len,
                                void* ws, size_t ws_bytes, cudaStream_t stream);
+
+/* Gradients of da2_cross_attention; out and lse are its results, dout the gradient of out.
+     D = sum_c dout out,  dS = p (dout v^T - D),
+     dq = sm_scale dS k,  dk = sm_scale dS^T q,  dv = p^T dout  (dk, dv summed over the query
+   heads that share a key/value head).
+   Every row of dq, dk and dv is written: zero for keys behind the length and for batch entries of
+   length 0. The sums run in a fixed order. ws as above, of the backward pass's own size. */
+da2_status da2_cross_attention_backward(const da2_cross_config* cfg, const da2_tensor* dout,
+                                        const da2_tensor* q, const da2_tensor* k, const da2_tensor* v,
+                                        const da2_tensor* out, const float* lse, const int32_t* kv_len,
+                                        const da2_tensor* dq, const da2_tensor* dk, const da2_tensor* dv,
+                                        void* ws, size_t ws_bytes, cudaStream_t stream);
 
 /* Reads the error word of a cross-attention workspace into *word and clears it (synchronises
    `stream`): DA2_ERR_TIMEOUT if it was non-zero. */

@@ -121,6 +121,7 @@ EXPORTED = ("da2_workspace_size", "da2_workspace_views", "da2_prepare", "da2_dra
             "da2_status_string", "da2_forward_noalloc", "da2_last_cuda_error",
             "da2_check_selection", "da2_qk_norm_rope", "da2_qk_norm_rope_workspace_size",
             "da2_qk_norm_rope_backward", "da2_cross_attention_workspace_size", "da2_cross_attention",
+            "da2_cross_attention_backward_workspace_size", "da2_cross_attention_backward",
             "da2_cross_attention_get_error")
 
 

@@ -53,6 +53,8 @@ SIGNATURES = {
     "da2_qk_norm_rope_backward": [_np, _tp, _tp, _tp, _tp, _vp, _vp, _vp, _vp, _tp, _tp, _vp, _vp, _vp, _sz, _vp],
     "da2_cross_attention_workspace_size": [_xp, _szp],
     "da2_cross_attention": [_xp, _tp, _tp, _tp, _tp, _vp, _vp, _vp, _sz, _vp],
+    "da2_cross_attention_backward_workspace_size": [_xp, _szp],
+    "da2_cross_attention_backward": [_xp, _tp, _tp, _tp, _tp, _tp, _vp, _vp, _tp, _tp, _tp, _vp, _sz, _vp],
     "da2_cross_attention_get_error": [_vp, _sz, _vp, ctypes.POINTER(ctypes.c_uint32)],
 }
 

@@ -12,7 +12,7 @@ CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libda2.so")
 LIB_DEBUG = os.path.join(HERE, "libda2_debug.so")   # DA2_DEBUG: blocking error checks, list checks
 SOURCES = ["da2_api.cu", "prep.cu", "draft.cu", "attn_tc.cu", "da2_noalloc.cu", "checks.cu",
-           "norm_rope.cu", "cross_api.cu", "cross_fwd.cu"]
+           "norm_rope.cu", "cross_api.cu", "cross_fwd.cu", "cross_bwd.cu"]
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 
 

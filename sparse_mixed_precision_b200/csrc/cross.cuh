@@ -98,6 +98,16 @@ __device__ __forceinline__ uint32_t pack16<__half>(float a, float b) {
   const __half2 h = __floats2half2_rn(a, b);
   return *reinterpret_cast<const uint32_t*>(&h);
 }
+template <typename T>
+__device__ __forceinline__ float2 unpack16(uint32_t u);
+template <>
+__device__ __forceinline__ float2 unpack16<__nv_bfloat16>(uint32_t u) {
+  return make_float2(__uint_as_float(u << 16), __uint_as_float(u & 0xFFFF0000u));
+}
+template <>
+__device__ __forceinline__ float2 unpack16<__half>(uint32_t u) {
+  return __half22float2(*reinterpret_cast<const __half2*>(&u));
+}
 
 // One 128-row tile of D channels as 64-channel boxes behind each other (128-byte swizzle). Rows
 // past the tensor's end are filled with zeros.

@@ -60,6 +60,19 @@ FwdLayout fwd_layout(const da2_cross_config* c) {
   return l;
 }
 
+struct BwdLayout {
+  size_t lse2, delta, part, total;
+};
+BwdLayout bwd_layout(const da2_cross_config* c) {
+  BwdLayout l;
+  const size_t rows = (size_t)c->B * c->H * (((size_t)c->Tq + 127) / 128 * 128);
+  l.lse2 = kErrBytes;
+  l.delta = l.lse2 + rows * 4;
+  l.part = l.delta + rows * 4;
+  l.total = l.part + (size_t)2 * kSms * 2 * c->d * 128 * 4;
+  return l;
+}
+
 typedef CUresult (*EncodeTiled)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
                                 const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
                                 CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
@@ -163,6 +176,52 @@ da2_status da2_cross_attention(const da2_cross_config* cfg, const da2_tensor* q,
   if (e == cudaSuccess) e = make_map(&m.k, in[1], cfg->B, cfg->Hkv, cfg->Tk, cfg->d, bf16);
   if (e == cudaSuccess) e = make_map(&m.v, in[2], cfg->B, cfg->Hkv, cfg->Tk, cfg->d, bf16);
   if (e == cudaSuccess) e = launch_cross_forward(g, m, bf16, stream);
+  return cuda_status(e);
+}
+
+da2_status da2_cross_attention_backward_workspace_size(const da2_cross_config* cfg, size_t* bytes) {
+  const da2_status s = check_cross_config(cfg);
+  if (s != DA2_OK) return s;
+  if (!bytes) return DA2_ERR_INVALID_ARG;
+  *bytes = bwd_layout(cfg).total;
+  return DA2_OK;
+}
+
+da2_status da2_cross_attention_backward(const da2_cross_config* cfg, const da2_tensor* dout,
+                                        const da2_tensor* q, const da2_tensor* k, const da2_tensor* v,
+                                        const da2_tensor* out, const float* lse, const int32_t* kv_len,
+                                        const da2_tensor* dq, const da2_tensor* dk, const da2_tensor* dv,
+                                        void* ws, size_t ws_bytes, cudaStream_t stream) {
+  const NvtxRange range("da2_cross_attention_backward");
+  da2_status s = check_cross_config(cfg);
+  if (s != DA2_OK) return s;
+  da2_tensor in[3];
+  CrossArgs g;
+  s = common_args(cfg, q, k, v, lse, kv_len, ws, in, &g);
+  if (s == DA2_OK) s = check_tensor(out, cfg->B, cfg->H, cfg->Tq, &g.out);
+  if (s == DA2_OK) s = check_tensor(dout, cfg->B, cfg->H, cfg->Tq, &g.dout);
+  if (s == DA2_OK) s = check_tensor(dq, cfg->B, cfg->H, cfg->Tq, &g.dq);
+  if (s == DA2_OK) s = check_tensor(dk, cfg->B, cfg->Hkv, cfg->Tk, &g.dk);
+  if (s == DA2_OK) s = check_tensor(dv, cfg->B, cfg->Hkv, cfg->Tk, &g.dv);
+  if (s != DA2_OK) return s;
+  if (!lse) return DA2_ERR_INVALID_ARG;
+  const BwdLayout l = bwd_layout(cfg);
+  if (ws_bytes < l.total) return DA2_ERR_WORKSPACE;
+  uint8_t* base = static_cast<uint8_t*>(ws);
+  g.lse_in = lse;
+  g.q_tiles = (cfg->Tq + 127) / 128;
+  g.k_tiles = (cfg->Tk + 127) / 128;
+  g.lse2 = reinterpret_cast<float*>(base + l.lse2);
+  g.delta = reinterpret_cast<float*>(base + l.delta);
+  g.part_kv = reinterpret_cast<float*>(base + l.part);
+  const bool bf16 = cfg->dtype == DA2_DTYPE_BF16;
+  CrossMaps m = {};
+  cudaError_t e = device_sms(&g.sms);
+  if (e == cudaSuccess) e = make_map(&m.q, in[0], cfg->B, cfg->H, cfg->Tq, cfg->d, bf16);
+  if (e == cudaSuccess) e = make_map(&m.k, in[1], cfg->B, cfg->Hkv, cfg->Tk, cfg->d, bf16);
+  if (e == cudaSuccess) e = make_map(&m.v, in[2], cfg->B, cfg->Hkv, cfg->Tk, cfg->d, bf16);
+  if (e == cudaSuccess) e = make_map(&m.dout, g.dout, cfg->B, cfg->H, cfg->Tq, cfg->d, bf16);
+  if (e == cudaSuccess) e = launch_cross_backward(g, m, bf16, stream);
   return cuda_status(e);
 }
 

@@ -1,0 +1,739 @@
+// Gradients of the attention to an encoder's states.
+//
+//   p = 2^(s log2e - lse2),  D = sum_c dout out,  dS = p (dout v^T - D)
+//   dq = scale dS k,  dk = scale dS^T q,  dv = p^T dout
+//
+// Two kernels without atomics, so that equal inputs give equal bits: k_cross_dq holds one query
+// tile and walks the keys; k_cross_dkv holds one key tile and walks the queries. Each recomputes
+// S and dP, which makes seven products of five; accumulating dq over key tiles in memory instead
+// would move 8 bytes per element and key tile, more time than the two products.
+//
+// p and dS are rounded once to the 16-bit type as MMA operands (fp32 accumulators). In fp16 both
+// carry a factor of 2^6, taken out of the accumulators: with many keys p and dS fall below fp16's
+// smallest normal 2^-14 otherwise, while |dS| stays in range up to 1023.
+#include <type_traits>
+
+#include "cross.cuh"
+#include "f32x2.cuh"
+
+namespace da2 {
+namespace {
+
+constexpr int kThreads = 384;
+constexpr int kMmaWarp = 8, kLoadWarp = 9, kCleanWarp = 10;
+
+template <typename T>
+struct Scale {
+  static constexpr bool kBf16 = std::is_same<T, __nv_bfloat16>::value;
+  static constexpr float kLog2 = kBf16 ? 0.0f : 6.0f;      // of p and dS
+  static constexpr float kInv = kBf16 ? 1.0f : 1.0f / 64.0f;
+};
+
+// All lanes' tensor-memory accesses before, one arrival per warp after.
+__device__ __forceinline__ void warp_arrive(uint64_t* bar, int lane) {
+  tc::fence_before_sync();
+  __syncwarp();
+  if (lane == 0) tc::mbar_arrive(bar);
+}
+__device__ __forceinline__ void tmem_ld64(uint32_t taddr, uint32_t* v) {
+  tc::tmem_ld32(taddr, v);
+  tc::tmem_ld32(taddr + 32, v + 32);
+#pragma unroll
+  for (int k = 0; k < 64; k += 16) tc::tmem_wait_ld16(v + k);
+}
+// 32 consecutive elements of a row, rounded and stored.
+template <typename T>
+__device__ __forceinline__ void store32(T* dst, const uint32_t* v, float f) {
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    uint32_t u[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      u[e] = pack16<T>(__uint_as_float(v[8 * k + 2 * e]) * f, __uint_as_float(v[8 * k + 2 * e + 1]) * f);
+    reinterpret_cast<uint4*>(dst)[k] = make_uint4(u[0], u[1], u[2], u[3]);
+  }
+}
+
+// ------------------------------------------------------------------------------------ dq
+// A work item is one 128-row query tile; Q and dout stay in shared memory, key and value tiles
+// come through a ring. 8 softmax warps share each 128 x 128 step: thread (w, r) owns row r and the
+// keys 64 w .. 64 w + 63. S and dP of the next step are multiplied as soon as this step's have been
+// read into registers. D is computed here (dout is in shared memory, out is read once) and left in
+// the workspace, with lse in the log2 domain, padded to whole tiles, for k_cross_dkv.
+template <int D>
+struct SmemDq {
+  static constexpr uint32_t kTile = 128 * D * 2;
+  static constexpr int kStages = D == 128 ? 5 : 8;
+  static constexpr uint32_t kDo = kTile, kStage0 = 2 * kTile;
+  static constexpr uint32_t kExch = kStage0 + kStages * kTile;      // [2 halves][128] fp32
+  static constexpr uint32_t kBars = kExch + 1024;
+  static constexpr uint32_t kBytes = kBars + 384 + 1024;
+  static_assert(kBytes <= 232448, "shared memory budget");
+};
+template <int D>
+struct BarsDq {
+  uint64_t kv_full[SmemDq<D>::kStages], kv_empty[SmemDq<D>::kStages];
+  uint64_t q_full, q_empty, s_full, s_free, dp_full, dp_free, ds_full[2], ds_free[2], dq_full, dq_free;
+  uint64_t k_dirty, k_clean, done;
+  uint32_t tmem, abort;
+};
+static_assert(sizeof(BarsDq<64>) <= 384, "barrier area");
+
+constexpr uint32_t kDqS = 0, kDqP = 128, kDqAcc = 256, kDqDs = 384;   // columns; dS: two of 64
+
+struct ItemDq {
+  int b, h, qt, nt, len;
+  __device__ __forceinline__ ItemDq(const CrossArgs& g, int i) {
+    qt = i % g.q_tiles;
+    i /= g.q_tiles;
+    b = i / g.H;
+    h = i - b * g.H;
+    len = valid_keys(g, b);
+    nt = (len + 127) >> 7;
+  }
+  __device__ __forceinline__ int keys(int t) const { return min(128, len - 128 * t); }
+  __device__ __forceinline__ bool dirty(const CrossArgs& g, int t) const {
+    return (keys(t) & 15) != 0 && len < g.Tk;
+  }
+};
+
+template <typename T, int D>
+__global__ void __launch_bounds__(kThreads, 1)
+k_cross_dq(const __grid_constant__ CrossMaps maps, const __grid_constant__ CrossArgs g) {
+  using S = SmemDq<D>;
+  constexpr int kStages = S::kStages;
+  constexpr bool kBf16 = Scale<T>::kBf16;
+  extern __shared__ uint8_t sm_raw[];
+  uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(sm_raw) + 1023) & ~uintptr_t(1023));
+  BarsDq<D>* bars = reinterpret_cast<BarsDq<D>*>(sm + S::kBars);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int items = g.B * g.H * g.q_tiles;
+  const Guard gd{g.err, &bars->abort, g.wait_ns};
+
+  if (tid == 0) {
+    for (int s = 0; s < kStages; ++s) {
+      tc::mbar_init(&bars->kv_full[s], 1);
+      tc::mbar_init(&bars->kv_empty[s], 1);
+    }
+    tc::mbar_init(&bars->q_full, 1);
+    tc::mbar_init(&bars->q_empty, 1 + 8);                // the MMAs, and the warps that read dout
+    tc::mbar_init(&bars->s_full, 1);
+    tc::mbar_init(&bars->s_free, 8);
+    tc::mbar_init(&bars->dp_full, 1);
+    tc::mbar_init(&bars->dp_free, 8);
+    for (int x = 0; x < 2; ++x) {
+      tc::mbar_init(&bars->ds_full[x], 8);
+      tc::mbar_init(&bars->ds_free[x], 1);
+    }
+    tc::mbar_init(&bars->dq_full, 1);
+    tc::mbar_init(&bars->dq_free, 8);
+    tc::mbar_init(&bars->k_dirty, 1);
+    tc::mbar_init(&bars->k_clean, 1);
+    tc::mbar_init(&bars->done, 1);
+    bars->abort = 0u;
+    tc::fence_mbar_init();
+  }
+  if (warp == kMmaWarp) {
+    tc::tmem_alloc(&bars->tmem, 512);
+    tc::tmem_relinquish();
+  }
+  tc::fence_before_sync();
+  __syncthreads();
+  tc::fence_after_sync();
+  const uint32_t tmem = bars->tmem;
+
+  if (warp == kLoadWarp) {
+    if (lane == 0) {
+      uint32_t n = 0, q_loads = 0;
+      bool dead = false;
+      auto load = [&](const CUtensorMap* map, int row, int head, int b) {
+        const uint32_t s = n % kStages;
+        if (g.stall && n == 0) { ++n; return true; }
+        if (!guard_wait(&bars->kv_empty[s], ((n / kStages) & 1) ^ 1, gd)) return false;
+        tc::mbar_arrive_expect_tx(&bars->kv_full[s], S::kTile);
+        load_tile<D>(sm + S::kStage0 + s * S::kTile, map, row, head, b, &bars->kv_full[s]);
+        ++n;
+        return true;
+      };
+      for (int i = blockIdx.x; i < items && !dead; i += gridDim.x) {
+        const ItemDq w(g, i);
+        if (w.nt == 0) continue;
+        if (!guard_wait(&bars->q_empty, (q_loads & 1) ^ 1, gd)) break;
+        tc::mbar_arrive_expect_tx(&bars->q_full, 2 * S::kTile);
+        load_tile<D>(sm, &maps.q, 128 * w.qt, w.h, w.b, &bars->q_full);
+        load_tile<D>(sm + S::kDo, &maps.dout, 128 * w.qt, w.h, w.b, &bars->q_full);
+        ++q_loads;
+        for (int t = 0; t < w.nt && !dead; ++t) {
+          dead = !load(&maps.k, 128 * t, w.h / g.group, w.b);
+          if (!dead) dead = !load(&maps.v, 128 * t, w.h / g.group, w.b);
+        }
+      }
+      for (uint32_t s = 0; s < (uint32_t)kStages && s < n; ++s)
+        guard_wait(&bars->kv_full[s], ((n - 1 - s) / kStages) & 1, gd, false);
+      if (q_loads) guard_wait(&bars->q_full, (q_loads - 1) & 1, gd, false);
+    }
+  } else if (warp == kMmaWarp) {
+    if (lane == 0) {
+      uint32_t step = 0, q_items = 0, acc_items = 0, cleans = 0;
+      const uint64_t dQ = tc::sdesc_k(sm), dDo = tc::sdesc_k(sm + S::kDo);
+      auto wait_stage = [&](uint32_t n) { return guard_wait(&bars->kv_full[n % kStages], (n / kStages) & 1, gd); };
+      auto product = [&](uint32_t acc, uint64_t a, const uint8_t* tile, int keys) {
+        const uint32_t id = tc::idesc_f16(kBf16, 128, (keys + 15) & ~15, false);
+        const uint64_t b = tc::sdesc_k(tile);
+#pragma unroll
+        for (int k = 0; k < D / 16; ++k) {
+          const uint64_t off = (k / 4) * (16384 >> 4) + (k % 4) * (32 >> 4);
+          tc::mma_f16(tmem + acc, a + off, b + off, id, k > 0);
+        }
+      };
+      auto issue_s = [&](const ItemDq& w, int t, uint32_t gs) -> bool {
+        if (gs > 0 && !guard_wait(&bars->s_free, (gs - 1) & 1, gd)) return false;
+        if (t == 0 && !guard_wait(&bars->q_full, q_items++ & 1, gd)) return false;
+        if (!wait_stage(2 * gs)) return false;
+        tc::fence_after_sync();
+        product(kDqS, dQ, sm + S::kStage0 + (2 * gs) % kStages * S::kTile, w.keys(t));
+        tc::mma_commit(&bars->s_full);
+        return true;
+      };
+      auto issue_dp = [&](const ItemDq& w, int t, uint32_t gs) -> bool {
+        if (gs > 0 && !guard_wait(&bars->dp_free, (gs - 1) & 1, gd)) return false;
+        const uint32_t n = 2 * gs + 1;
+        if (!wait_stage(n)) return false;
+        tc::fence_after_sync();
+        product(kDqP, dDo, sm + S::kStage0 + n % kStages * S::kTile, w.keys(t));
+        tc::mma_commit(&bars->dp_full);
+        tc::mma_commit(&bars->kv_empty[n % kStages]);
+        if (t == w.nt - 1) tc::mma_commit(&bars->q_empty);
+        return true;
+      };
+      auto issue_dq = [&](const ItemDq& w, int t, uint32_t gs) -> bool {
+        if (w.dirty(g, t)) tc::mbar_arrive(&bars->k_dirty);      // landed long ago: S has read it
+        if (!guard_wait(&bars->ds_full[gs & 1], (gs >> 1) & 1, gd)) return false;
+        if (w.dirty(g, t) && !guard_wait(&bars->k_clean, cleans++ & 1, gd)) return false;
+        if (t == 0) {
+          if (acc_items > 0 && !guard_wait(&bars->dq_free, (acc_items - 1) & 1, gd)) return false;
+          ++acc_items;
+        }
+        tc::fence_after_sync();
+        const uint32_t s = (2 * gs) % kStages, id = tc::idesc_f16(kBf16, 128, D, true);
+        const uint64_t b = tc::sdesc_mn(sm + S::kStage0 + s * S::kTile, 16384);
+        const int ks = (w.keys(t) + 15) >> 4;
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+          if (k < ks)
+            tc::mma_f16_ta(tmem + kDqAcc, tmem + kDqDs + 64 * (gs & 1) + 8 * k, b + k * (2048 >> 4), id,
+                           (t > 0) | (k > 0));
+        tc::mma_commit(&bars->kv_empty[s]);
+        tc::mma_commit(&bars->ds_free[gs & 1]);
+        if (t == w.nt - 1) tc::mma_commit(&bars->dq_full);
+        return true;
+      };
+      auto skip_empty = [&](int at) {
+        while (at < items && ItemDq(g, at).nt == 0) at += gridDim.x;
+        return at;
+      };
+      int i = skip_empty(blockIdx.x);
+      if (i < items) {
+        ItemDq w(g, i);
+        bool dead = !issue_s(w, 0, 0) || !issue_dp(w, 0, 0);
+        while (!dead) {
+          const int in = skip_empty(i + gridDim.x);
+          const bool more = in < items;
+          const ItemDq wn(g, more ? in : i);
+          for (int t = 0; t < w.nt && !dead; ++t, ++step) {
+            const bool last = t == w.nt - 1;
+            if (!last) dead = !issue_s(w, t + 1, step + 1) || !issue_dp(w, t + 1, step + 1);
+            else if (more) dead = !issue_s(wn, 0, step + 1) || !issue_dp(wn, 0, step + 1);
+            if (!dead) dead = !issue_dq(w, t, step);
+          }
+          if (!more) break;
+          w = wn;
+          i = in;
+        }
+      }
+      tc::mma_commit(&bars->done);
+      guard_wait(&bars->done, 0, gd, false);
+    }
+  } else if (warp == kCleanWarp) {
+    uint32_t step = 0, cleans = 0;
+    for (int i = blockIdx.x; i < items; i += gridDim.x) {
+      const ItemDq w(g, i);
+      if (w.nt > 0 && w.dirty(g, w.nt - 1)) {
+        if (!guard_wait(&bars->k_dirty, cleans++ & 1, gd)) break;
+        const int keys = w.keys(w.nt - 1);
+        zero_rows<D>(sm + S::kStage0 + (2 * (step + w.nt - 1)) % kStages * S::kTile, keys, (keys + 15) & ~15, lane);
+        if (lane == 0) tc::mbar_arrive(&bars->k_clean);
+      }
+      step += w.nt;
+    }
+  } else if (warp < kMmaWarp) {
+    const int half = warp >> 2, r = tid & 127;
+    const uint32_t lane_base = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+    const float c = g.scale_log2;
+    uint32_t step = 0, n_items = 0;
+    for (int i = blockIdx.x; i < items; i += gridDim.x) {
+      const ItemDq w(g, i);
+      const int row = 128 * w.qt + r;
+      const bool on = row < g.Tq;
+      T* dq = static_cast<T*>(g.dq.data) + w.b * g.dq.sb + w.h * g.dq.sh + row * g.dq.st + half * (D / 2);
+      if (w.nt == 0) {
+        if (on)
+          for (int k = 0; k < D / 16; ++k) reinterpret_cast<uint4*>(dq)[k] = make_uint4(0u, 0u, 0u, 0u);
+        continue;
+      }
+      // D: this thread's half of the row of dout (swizzled in shared memory) and of out
+      const size_t bh = (size_t)w.b * g.H + w.h;
+      const float lse2 = on ? g.lse_in[bh * g.Tq + row] * kLog2E : INFINITY;
+      uint4 o[D / 16];
+      const T* op = static_cast<const T*>(g.out.data) + w.b * g.out.sb + w.h * g.out.sh + row * g.out.st + half * (D / 2);
+#pragma unroll
+      for (int k = 0; k < D / 16; ++k) o[k] = on ? __ldg(reinterpret_cast<const uint4*>(op) + k) : make_uint4(0u, 0u, 0u, 0u);
+      if (!guard_wait(&bars->q_full, n_items & 1, gd)) break;
+      float part = 0.0f;
+#pragma unroll
+      for (int k = 0; k < D / 16; ++k) {
+        const int ch = half * (D / 16) + k;              // 16-byte chunk of the row
+        const uint4 u = *reinterpret_cast<const uint4*>(sm + S::kDo + (ch >> 3) * 16384 + r * 128 +
+                                                        (((ch & 7) ^ (r & 7)) << 4));
+        const uint32_t a[4] = {u.x, u.y, u.z, u.w}, b[4] = {o[k].x, o[k].y, o[k].z, o[k].w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float2 x = unpack16<T>(a[e]), y = unpack16<T>(b[e]);
+          part = fmaf(x.x, y.x, fmaf(x.y, y.y, part));
+        }
+      }
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(&bars->q_empty);
+      float* exch = reinterpret_cast<float*>(sm + S::kExch);
+      exch[half * 128 + r] = part;
+      asm volatile("bar.sync 1, 256;" ::: "memory");
+      const float delta = exch[r] + exch[128 + r];
+      asm volatile("bar.sync 1, 256;" ::: "memory");     // read by all before the next item writes
+      if (half == 0) {
+        const size_t at = bh * (128 * (size_t)g.q_tiles) + row;
+        g.lse2[at] = lse2;
+        g.delta[at] = delta;
+      }
+      const f32x2 c2 = pk2(c, c), b2 = pk2(Scale<T>::kLog2 - lse2, Scale<T>::kLog2 - lse2), d2 = pk2(-delta, -delta);
+      for (int t = 0; t < w.nt; ++t, ++step) {
+        const int keys = w.keys(t) - 64 * half;          // of this thread's 64
+        guard_wait(&bars->s_full, step & 1, gd);
+        tc::fence_after_sync();
+        uint32_t su[64], pu[64];
+        float* s = reinterpret_cast<float*>(su);
+        float* p = reinterpret_cast<float*>(pu);
+        tmem_ld64(lane_base + kDqS + 64 * half, su);
+        warp_arrive(&bars->s_free, lane);
+#pragma unroll
+        for (int k = 0; k < 64; k += 2) {
+          float x, y;
+          upk2(fma2(pk2(s[k], s[k + 1]), c2, b2), x, y);
+          s[k] = ex2(x);
+          s[k + 1] = ex2(y);
+        }
+        guard_wait(&bars->dp_full, step & 1, gd);
+        tc::fence_after_sync();
+        tmem_ld64(lane_base + kDqP + 64 * half, pu);
+        warp_arrive(&bars->dp_free, lane);
+        uint32_t ds[32];
+#pragma unroll
+        for (int k = 0; k < 64; k += 2) {
+          float x, y;
+          upk2(mul2(add2(pk2(p[k], p[k + 1]), d2), pk2(s[k], s[k + 1])), x, y);
+          if (k >= keys) x = 0.0f;                       // also NaN from behind the length
+          if (k + 1 >= keys) y = 0.0f;
+          ds[k >> 1] = pack16<T>(x, y);
+        }
+        if (step >= 2) {
+          guard_wait(&bars->ds_free[step & 1], ((step >> 1) - 1) & 1, gd);
+          tc::fence_after_sync();
+        }
+        tc::tmem_st16(lane_base + kDqDs + 64 * (step & 1) + 32 * half, ds);
+        tc::tmem_st16(lane_base + kDqDs + 64 * (step & 1) + 32 * half + 16, ds + 16);
+        tc::tmem_wait_st();
+        warp_arrive(&bars->ds_full[step & 1], lane);
+      }
+      if (!guard_wait(&bars->dq_full, n_items & 1, gd)) break;
+      tc::fence_after_sync();
+      uint32_t acc[D / 2];
+#pragma unroll
+      for (int k = 0; k < D / 2; k += 32) tc::tmem_ld32(lane_base + kDqAcc + half * (D / 2) + k, acc + k);
+#pragma unroll
+      for (int k = 0; k < D / 2; k += 16) tc::tmem_wait_ld16(acc + k);
+      warp_arrive(&bars->dq_free, lane);
+      if (on) {
+#pragma unroll
+        for (int k = 0; k < D / 2; k += 32) store32<T>(dq + k, acc + k, g.scale * Scale<T>::kInv);
+      }
+      ++n_items;
+    }
+  }
+  tc::fence_before_sync();
+  __syncthreads();
+  if (warp == kMmaWarp) {
+    tc::fence_after_sync();
+    tc::tmem_dealloc(tmem, 512);
+  }
+}
+
+// ------------------------------------------------------------------------------------ dk, dv
+// A group is one key tile of one key/value head; its units are the query tiles of all query heads
+// that share the head. The groups with a valid key, laid end to end, are cut into one run of units
+// per block: a run that covers a group writes dk and dv, the ends of a group that blocks share go
+// to the workspace as fp32 parts, two per block at most, and k_cross_dkv_join adds them in order.
+// Transposed products: S^T = K Q^T and dP^T = V dout^T (key rows in the tensor-memory lanes), P^T
+// and dS^T overwrite them as 16-bit A operands of dv += P^T dout and dk += dS^T Q, each next S and dP
+// issued directly behind. Key rows behind the length only reach their own rows of dk and dv, which
+// are written as zero.
+template <int D>
+struct SmemDkv {
+  static constexpr uint32_t kTile = 128 * D * 2;
+  static constexpr int kStages = D == 128 ? 4 : 8;       // even: dout behind Q
+  static constexpr uint32_t kV = kTile, kStage0 = 2 * kTile;
+  static constexpr uint32_t kVec = kStage0 + kStages * kTile;       // per Q stage: lse2[128], delta[128]
+  static constexpr uint32_t kBars = kVec + kStages / 2 * 1024;
+  static constexpr uint32_t kBytes = kBars + 512 + 1024;
+  static_assert(kBytes <= 232448, "shared memory budget");
+};
+template <int D>
+struct BarsDkv {
+  uint64_t q_full[SmemDkv<D>::kStages], q_empty[SmemDkv<D>::kStages];
+  uint64_t kv_full, kv_empty, s_full, p_full, dp_full, ds_full, acc_full, acc_free, done;
+  uint32_t tmem, abort;
+};
+static_assert(sizeof(BarsDkv<64>) <= 512, "barrier area");
+
+constexpr uint32_t kKvS = 0, kKvP = 128, kKvDv = 256, kKvDk = 384;    // columns
+
+// The live groups and how the blocks share them.
+struct Share {
+  long units;                 // of all live groups
+  int n;                      // units per group
+  int blocks;
+  __device__ __forceinline__ Share(const CrossArgs& g) {
+    long live = 0;
+    for (int b = 0; b < g.B; ++b) live += (valid_keys(g, b) + 127) >> 7;
+    n = g.group * g.q_tiles;
+    units = live * g.Hkv * n;
+    blocks = g.sms;
+  }
+  __device__ __forceinline__ long begin(int c) const { return units * c / blocks; }
+};
+// Live group i: batch entry, key/value head, key tile.
+struct Group {
+  int b, hkv, kt, len;
+  __device__ __forceinline__ Group(const CrossArgs& g, long i) {
+    for (b = 0;; ++b) {
+      len = valid_keys(g, b);
+      const int tiles = (len + 127) >> 7;
+      const long here = (long)tiles * g.Hkv;
+      if (i < here || b == g.B - 1) {
+        hkv = (int)(i / max(tiles, 1));
+        kt = (int)(i - (long)hkv * tiles);
+        return;
+      }
+      i -= here;
+    }
+  }
+};
+
+template <typename T, int D>
+__global__ void __launch_bounds__(kThreads, 1)
+k_cross_dkv(const __grid_constant__ CrossMaps maps, const __grid_constant__ CrossArgs g) {
+  using S = SmemDkv<D>;
+  constexpr int kStages = S::kStages;
+  constexpr bool kBf16 = Scale<T>::kBf16;
+  extern __shared__ uint8_t sm_raw[];
+  uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(sm_raw) + 1023) & ~uintptr_t(1023));
+  BarsDkv<D>* bars = reinterpret_cast<BarsDkv<D>*>(sm + S::kBars);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const Guard gd{g.err, &bars->abort, g.wait_ns};
+
+  if (tid == 0) {
+    for (int s = 0; s < kStages; ++s) {
+      tc::mbar_init(&bars->q_full[s], 1);
+      tc::mbar_init(&bars->q_empty[s], 1);
+    }
+    tc::mbar_init(&bars->kv_full, 1);
+    tc::mbar_init(&bars->kv_empty, 1);
+    tc::mbar_init(&bars->s_full, 1);
+    tc::mbar_init(&bars->p_full, 8);
+    tc::mbar_init(&bars->dp_full, 1);
+    tc::mbar_init(&bars->ds_full, 8);
+    tc::mbar_init(&bars->acc_full, 1);
+    tc::mbar_init(&bars->acc_free, 8);
+    tc::mbar_init(&bars->done, 1);
+    bars->abort = 0u;
+    tc::fence_mbar_init();
+  }
+  if (warp == kMmaWarp) {
+    tc::tmem_alloc(&bars->tmem, 512);
+    tc::tmem_relinquish();
+  }
+  tc::fence_before_sync();
+  __syncthreads();
+  tc::fence_after_sync();
+  const uint32_t tmem = bars->tmem;
+  const Share sh(g);
+  const long u0 = sh.begin(blockIdx.x), u1 = sh.begin(blockIdx.x + 1);
+
+  if (warp == kLoadWarp) {
+    if (lane == 0) {
+      uint32_t n = 0, groups = 0;
+      bool dead = false;
+      for (long u = u0; u < u1 && !dead;) {
+        const long gi = u / sh.n;
+        const Group w(g, gi);
+        const int e = (int)(min(u1, (gi + 1) * sh.n) - gi * sh.n);
+        if (!guard_wait(&bars->kv_empty, (groups & 1) ^ 1, gd)) break;
+        tc::mbar_arrive_expect_tx(&bars->kv_full, 2 * S::kTile);
+        load_tile<D>(sm, &maps.k, 128 * w.kt, w.hkv, w.b, &bars->kv_full);
+        load_tile<D>(sm + S::kV, &maps.v, 128 * w.kt, w.hkv, w.b, &bars->kv_full);
+        ++groups;
+        for (int i = (int)(u - gi * sh.n); i < e && !dead; ++i) {
+          const int h = w.hkv * g.group + i / g.q_tiles, qt = i % g.q_tiles;
+          for (int x = 0; x < 2; ++x) {                  // Q with its two vectors, then dout
+            const uint32_t s = n % kStages;
+            if (g.stall && n == 0) { ++n; continue; }
+            if (!guard_wait(&bars->q_empty[s], ((n / kStages) & 1) ^ 1, gd)) { dead = true; break; }
+            tc::mbar_arrive_expect_tx(&bars->q_full[s], S::kTile + (x == 0 ? 1024 : 0));
+            load_tile<D>(sm + S::kStage0 + s * S::kTile, x == 0 ? &maps.q : &maps.dout, 128 * qt, h, w.b,
+                         &bars->q_full[s]);
+            if (x == 0) {
+              const size_t at = (((size_t)w.b * g.H + h) * g.q_tiles + qt) * 128;
+              uint8_t* vec = sm + S::kVec + s / 2 * 1024;
+              tc::bulk_g2s(vec, g.lse2 + at, 512, &bars->q_full[s]);
+              tc::bulk_g2s(vec + 512, g.delta + at, 512, &bars->q_full[s]);
+            }
+            ++n;
+          }
+        }
+        u = gi * sh.n + e;
+      }
+      for (uint32_t s = 0; s < (uint32_t)kStages && s < n; ++s)
+        guard_wait(&bars->q_full[s], ((n - 1 - s) / kStages) & 1, gd, false);
+      if (groups) guard_wait(&bars->kv_full, (groups - 1) & 1, gd, false);
+    }
+  } else if (warp == kMmaWarp) {
+    if (lane == 0 && u0 < u1) {
+      uint32_t groups = 0, accs = 0;
+      const uint64_t dK = tc::sdesc_k(sm), dV = tc::sdesc_k(sm + S::kV);
+      const uint32_t id_s = tc::idesc_f16(kBf16, 128, 128, false), id_o = tc::idesc_f16(kBf16, 128, D, true);
+      auto tile = [&](uint32_t n) { return sm + S::kStage0 + n % kStages * S::kTile; };
+      auto wait_stage = [&](uint32_t n) { return guard_wait(&bars->q_full[n % kStages], (n / kStages) & 1, gd); };
+      auto product = [&](uint32_t acc, uint64_t a, const uint8_t* t) {
+        const uint64_t b = tc::sdesc_k(t);
+#pragma unroll
+        for (int k = 0; k < D / 16; ++k) {
+          const uint64_t off = (k / 4) * (16384 >> 4) + (k % 4) * (32 >> 4);
+          tc::mma_f16(tmem + acc, a + off, b + off, id_s, k > 0);
+        }
+      };
+      // acc += A^T tile, A the 16-bit operand in the two 32-column halves behind col and col + 64
+      auto accumulate = [&](uint32_t acc, uint32_t col, const uint8_t* t, bool first) {
+        const uint64_t b = tc::sdesc_mn(t, 16384);
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+          tc::mma_f16_ta(tmem + acc, tmem + col + 64 * (k >> 2) + 8 * (k & 3), b + k * (2048 >> 4), id_o,
+                         !first | (k > 0));
+      };
+      auto issue_s = [&](bool new_group, uint32_t gs) -> bool {
+        if (new_group && !guard_wait(&bars->kv_full, groups++ & 1, gd)) return false;
+        if (!wait_stage(2 * gs)) return false;
+        tc::fence_after_sync();
+        product(kKvS, dK, tile(2 * gs));
+        tc::mma_commit(&bars->s_full);
+        return true;
+      };
+      auto issue_dp = [&](bool last_of_group, uint32_t gs) -> bool {
+        if (!wait_stage(2 * gs + 1)) return false;
+        tc::fence_after_sync();
+        product(kKvP, dV, tile(2 * gs + 1));
+        tc::mma_commit(&bars->dp_full);
+        if (last_of_group) tc::mma_commit(&bars->kv_empty);
+        return true;
+      };
+      // unit u is the last of its run within a group
+      auto ends = [&](long u) { return u + 1 == u1 || (u + 1) % sh.n == 0; };
+      bool dead = !issue_s(true, 0) || !issue_dp(ends(u0), 0);
+      bool first = true;
+      uint32_t step = 0;
+      for (long u = u0; u < u1 && !dead; ++u, ++step) {
+        const bool last = ends(u), more = u + 1 < u1;
+        if (!guard_wait(&bars->p_full, step & 1, gd)) break;
+        if (first && accs > 0 && !guard_wait(&bars->acc_free, (accs - 1) & 1, gd)) break;
+        tc::fence_after_sync();
+        accumulate(kKvDv, kKvS, tile(2 * step + 1), first);
+        tc::mma_commit(&bars->q_empty[(2 * step + 1) % kStages]);
+        if (more && !issue_s(last, step + 1)) break;
+        if (!guard_wait(&bars->ds_full, step & 1, gd)) break;
+        tc::fence_after_sync();
+        accumulate(kKvDk, kKvP, tile(2 * step), first);
+        tc::mma_commit(&bars->q_empty[(2 * step) % kStages]);
+        if (last) {
+          tc::mma_commit(&bars->acc_full);
+          ++accs;
+        }
+        if (more && !issue_dp(ends(u + 1), step + 1)) break;
+        first = last;
+      }
+      tc::mma_commit(&bars->done);
+      guard_wait(&bars->done, 0, gd, false);
+    }
+  } else if (warp < kMmaWarp) {
+    const int half = warp >> 2, r = tid & 127;
+    const uint32_t lane_base = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+    const f32x2 c2 = pk2(g.scale_log2, g.scale_log2);
+    const f32x2 k2 = pk2(Scale<T>::kLog2, Scale<T>::kLog2);
+    uint32_t step = 0, accs = 0;
+    bool dead = false;
+    for (long u = u0; u < u1 && !dead; ++accs) {
+      const long gi = u / sh.n;
+      const long end = min(u1, (gi + 1) * sh.n);
+      const bool whole = u == gi * sh.n && end == (gi + 1) * sh.n;
+      const int slot = 2 * blockIdx.x + (u == u0 ? 0 : 1);
+      for (; u < end; ++u, ++step) {
+        const uint32_t n = 2 * step, st = n % kStages;
+        const float4* vec = reinterpret_cast<const float4*>(sm + S::kVec + st / 2 * 1024 + half * 256);
+        guard_wait(&bars->q_full[st], (n / kStages) & 1, gd);      // the two vectors
+        guard_wait(&bars->s_full, step & 1, gd);
+        tc::fence_after_sync();
+        uint32_t su[64];
+        float* s = reinterpret_cast<float*>(su);
+        tmem_ld64(lane_base + kKvS + 64 * half, su);
+        uint32_t w16[32];
+#pragma unroll
+        for (int k = 0; k < 64; k += 4) {
+          const float4 l = vec[k / 4];
+          float x0, x1, x2, x3;
+          upk2(fma2(pk2(s[k], s[k + 1]), c2, add2(k2, pk2(-l.x, -l.y))), x0, x1);
+          upk2(fma2(pk2(s[k + 2], s[k + 3]), c2, add2(k2, pk2(-l.z, -l.w))), x2, x3);
+          s[k] = ex2(x0);
+          s[k + 1] = ex2(x1);
+          s[k + 2] = ex2(x2);
+          s[k + 3] = ex2(x3);
+          w16[k / 2] = pack16<T>(s[k], s[k + 1]);
+          w16[k / 2 + 1] = pack16<T>(s[k + 2], s[k + 3]);
+        }
+        tc::tmem_st16(lane_base + kKvS + 64 * half, w16);
+        tc::tmem_st16(lane_base + kKvS + 64 * half + 16, w16 + 16);
+        tc::tmem_wait_st();
+        warp_arrive(&bars->p_full, lane);
+        guard_wait(&bars->dp_full, step & 1, gd);
+        tc::fence_after_sync();
+        uint32_t pu[64];
+        float* p = reinterpret_cast<float*>(pu);
+        tmem_ld64(lane_base + kKvP + 64 * half, pu);
+#pragma unroll
+        for (int k = 0; k < 64; k += 4) {
+          const float4 d = vec[32 + k / 4];
+          float x0, x1, x2, x3;
+          upk2(mul2(add2(pk2(p[k], p[k + 1]), pk2(-d.x, -d.y)), pk2(s[k], s[k + 1])), x0, x1);
+          upk2(mul2(add2(pk2(p[k + 2], p[k + 3]), pk2(-d.z, -d.w)), pk2(s[k + 2], s[k + 3])), x2, x3);
+          w16[k / 2] = pack16<T>(x0, x1);
+          w16[k / 2 + 1] = pack16<T>(x2, x3);
+        }
+        tc::tmem_st16(lane_base + kKvP + 64 * half, w16);
+        tc::tmem_st16(lane_base + kKvP + 64 * half + 16, w16 + 16);
+        tc::tmem_wait_st();
+        warp_arrive(&bars->ds_full, lane);
+      }
+      // the accumulators: warps 0-3 dv, warps 4-7 dk
+      if (!guard_wait(&bars->acc_full, accs & 1, gd)) { dead = true; break; }
+      tc::fence_after_sync();
+      const Group w(g, gi);
+      const int key = 128 * w.kt + r;
+      const float f = (half ? g.scale : 1.0f) * Scale<T>::kInv;
+      const da2_tensor& out = half ? g.dk : g.dv;
+      T* row = static_cast<T*>(out.data) + w.b * out.sb + w.hkv * out.sh + key * out.st;
+      float* part = g.part_kv + ((size_t)slot * 2 + half) * D * 128 + r;
+#pragma unroll
+      for (int k0 = 0; k0 < D; k0 += 32) {
+        uint32_t v[32];
+        tc::tmem_ld32(lane_base + (half ? kKvDk : kKvDv) + k0, v);
+        tc::tmem_wait_ld16(v);
+        tc::tmem_wait_ld16(v + 16);
+        if (k0 + 32 == D) warp_arrive(&bars->acc_free, lane);
+        if (key >= w.len) {
+#pragma unroll
+          for (int k = 0; k < 32; ++k) v[k] = 0u;
+        }
+        if (!whole) {
+#pragma unroll
+          for (int k = 0; k < 32; ++k) part[(k0 + k) * 128] = __uint_as_float(v[k]) * f;
+        } else if (key < g.Tk) {
+          store32<T>(row + k0, v, f);
+        }
+      }
+    }
+  }
+  tc::fence_before_sync();
+  __syncthreads();
+  if (warp == kMmaWarp) {
+    tc::fence_after_sync();
+    tc::tmem_dealloc(tmem, 512);
+  }
+}
+
+// Adds the parts of one group's dv (y = 0) or dk (y = 1), 32 channels (z) at a time, in the order of
+// the blocks; groups that one block covered are done already. Groups without a valid key are zero.
+template <typename T, int D>
+__global__ void __launch_bounds__(128) k_cross_dkv_join(const __grid_constant__ CrossArgs g) {
+  const int kt = blockIdx.x % g.k_tiles, bh = blockIdx.x / g.k_tiles;
+  const int b = bh / g.Hkv, hkv = bh - b * g.Hkv, which = blockIdx.y, c0 = blockIdx.z * 32;
+  const int key = 128 * kt + threadIdx.x;
+  const int tiles = (valid_keys(g, b) + 127) >> 7;
+  float acc[32];
+#pragma unroll
+  for (int k = 0; k < 32; ++k) acc[k] = 0.0f;
+  if (kt < tiles) {
+    const Share sh(g);
+    long gi = (long)hkv * tiles + kt;
+    for (int i = 0; i < b; ++i) gi += (long)((valid_keys(g, i) + 127) >> 7) * g.Hkv;
+    const long a = gi * sh.n, e = a + sh.n;
+    int c = (int)(a * sh.blocks / sh.units);             // a block at or next to the first
+    while (c > 0 && sh.begin(c) > a) --c;
+    while (sh.begin(c + 1) <= a) ++c;
+    if (sh.begin(c + 1) >= e) return;                    // one block covered the group
+    for (; sh.begin(c) < e; ++c) {
+      if (sh.begin(c) == sh.begin(c + 1)) continue;
+      const int slot = 2 * c + (sh.begin(c) >= a ? 0 : 1);
+      const float* part = g.part_kv + ((size_t)slot * 2 + which) * D * 128 + (size_t)c0 * 128 + threadIdx.x;
+#pragma unroll
+      for (int k = 0; k < 32; ++k) acc[k] += part[k * 128];
+      if (c + 1 >= sh.blocks) break;
+    }
+  }
+  if (key >= g.Tk) return;
+  const da2_tensor& out = which ? g.dk : g.dv;
+  T* row = static_cast<T*>(out.data) + b * out.sb + hkv * out.sh + key * out.st + c0;
+  store32<T>(row, reinterpret_cast<const uint32_t*>(acc), 1.0f);
+}
+
+template <typename T, int D>
+cudaError_t launch(const CrossArgs& g, const CrossMaps& m, cudaStream_t st) {
+  cudaError_t e = cudaFuncSetAttribute(k_cross_dq<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       (int)SmemDq<D>::kBytes);
+  if (e == cudaSuccess)
+    e = cudaFuncSetAttribute(k_cross_dkv<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             (int)SmemDkv<D>::kBytes);
+  if (e != cudaSuccess) return e;
+  const int items = g.B * g.H * g.q_tiles;
+  k_cross_dq<T, D><<<items < g.sms ? items : g.sms, kThreads, SmemDq<D>::kBytes, st>>>(m, g);
+  e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  k_cross_dkv<T, D><<<g.sms, kThreads, SmemDkv<D>::kBytes, st>>>(m, g);
+  e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  k_cross_dkv_join<T, D><<<dim3((unsigned)(g.B * g.Hkv * g.k_tiles), 2, D / 32), 128, 0, st>>>(g);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_cross_backward(const CrossArgs& g, const CrossMaps& m, bool bf16, cudaStream_t st) {
+  if (g.d == 128) return bf16 ? launch<__nv_bfloat16, 128>(g, m, st) : launch<__half, 128>(g, m, st);
+  return bf16 ? launch<__nv_bfloat16, 64>(g, m, st) : launch<__half, 64>(g, m, st);
+}
+
+}  // namespace da2
