@@ -23,7 +23,7 @@ struct CrossArgs {
   float scale, scale_log2;         // softmax scale, and times log2(e)
   const int32_t* kv_len;           // null: Tk
   uint32_t* err;
-  unsigned long long wait_ns;
+  long long wait_clocks;           // limit of every bounded device wait
   int stall;                       // test hook: the first load is withheld
   int sms;                         // processors of the device
   // forward
@@ -39,8 +39,9 @@ struct CrossArgs {
   float* part_kv;                  // fp32 [2 sms][2][d][128]: dK and dV of split sums
 };
 
+// Boxes of 64 channels and 128 rows.
 struct CrossMaps {
-  CUtensorMap q, k, v, dout;
+  CUtensorMap q, k, v, dout, out;
 };
 
 cudaError_t launch_cross_forward(const CrossArgs& g, const CrossMaps& m, bool bf16, cudaStream_t st);
@@ -49,34 +50,41 @@ cudaError_t launch_cross_backward(const CrossArgs& g, const CrossMaps& m, bool b
 // ---------------------------------------------------------------- device helpers
 
 // A kernel's bounded waits: a wait that runs out sets the error word and the block's abort flag;
-// from then on every wait of the block returns false at once.
+// from then on every wait of the block returns false at once. A short inline part (one suspending
+// try), because the code of all of a kernel's waits competes with its loops for the instruction cache.
 struct Guard {
   uint32_t* err;
   volatile uint32_t* abort;        // shared memory, starts at zero
-  unsigned long long limit_ns;
+  long long limit;                 // clock cycles
 };
-__device__ __forceinline__ uint64_t global_ns() {
-  uint64_t t;
-  asm volatile("mov.u64 %0, %globaltimer;" : "=l"(t));
-  return t;
-}
-static __device__ __noinline__ bool guard_wait_slow(uint64_t* bar, uint32_t parity, const Guard& gd, bool honour_abort) {
-  const uint64_t t0 = global_ns();
-  while (true) {
-    for (int i = 0; i < 32; ++i)
-      if (tc::mbar_try_wait(bar, parity)) return true;
-    if (honour_abort && *gd.abort) return false;
-    if (global_ns() - t0 > gd.limit_ns) {
-      set_error(gd.err, kErrWaitTimeout);
-      *gd.abort = 1u;
+constexpr uint32_t kWaitNs = 20000;    // suspension per try
+static __device__ __noinline__ bool guard_wait_slow(uint64_t* bar, uint32_t parity, uint32_t* err,
+                                                    volatile uint32_t* abort, long long limit, bool honour_abort) {
+  const long long t0 = clock64();
+  while (!tc::mbar_try_wait_for(bar, parity, kWaitNs)) {
+    if (honour_abort && *abort) return false;
+    if (clock64() - t0 > limit) {
+      set_error(err, kErrWaitTimeout);
+      *abort = 1u;
       return false;
     }
   }
+  return true;
 }
 __device__ __forceinline__ bool guard_wait(uint64_t* bar, uint32_t parity, const Guard& gd,
                                            bool honour_abort = true) {
-  if (tc::mbar_test_wait(bar, parity)) return true;
-  return guard_wait_slow(bar, parity, gd, honour_abort);
+  if (tc::mbar_try_wait_for(bar, parity, kWaitNs)) return true;
+  return guard_wait_slow(bar, parity, gd.err, gd.abort, gd.limit, honour_abort);
+}
+// For a warp that stops when the wait fails: all lanes get the same answer.
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, const Guard& gd) {
+  return __all_sync(0xffffffffu, guard_wait(bar, parity, gd));
+}
+// All lanes' tensor-memory accesses before, one arrival per warp after.
+__device__ __forceinline__ void warp_arrive(uint64_t* bar, int lane) {
+  tc::fence_before_sync();
+  __syncwarp();
+  if (lane == 0) tc::mbar_arrive(bar);
 }
 
 __device__ __forceinline__ int valid_keys(const CrossArgs& g, int b) {
@@ -109,22 +117,22 @@ __device__ __forceinline__ float2 unpack16<__half>(uint32_t u) {
   return __half22float2(*reinterpret_cast<const __half2*>(&u));
 }
 
-// One 128-row tile of D channels as 64-channel boxes behind each other (128-byte swizzle). Rows
+// One tile of 128 rows and D channels as 64-channel boxes behind each other (128-byte swizzle). Rows
 // past the tensor's end are filled with zeros.
-template <int D>
+template <int D, int Rows = 128>
 __device__ __forceinline__ void load_tile(uint8_t* dst, const CUtensorMap* map, int row, int head, int b,
                                           uint64_t* bar) {
 #pragma unroll
-  for (int x = 0; x < D / 64; ++x) tc::tma_load_4d(dst + x * 16384, map, 64 * x, row, head, b, bar);
+  for (int x = 0; x < D / 64; ++x) tc::tma_load_4d(dst + x * Rows * 128, map, 64 * x, row, head, b, bar);
 }
 
-// Zeroes rows [r0, r1) of a tile in shared memory (whole rows, so the swizzle does not matter) for
-// the tensor cores to read. Called by a full warp.
-template <int D>
+// Zeroes rows [r0, r1) of such a tile in shared memory (whole rows, so the swizzle does not matter)
+// for the tensor cores to read. Called by a full warp.
+template <int D, int Rows = 128>
 __device__ __forceinline__ void zero_rows(uint8_t* tile, int r0, int r1, int lane) {
   for (int i = lane; i < (r1 - r0) * 8 * (D / 64); i += 32) {
     const int x = i / ((r1 - r0) * 8), o = i - x * (r1 - r0) * 8;
-    *reinterpret_cast<uint4*>(tile + x * 16384 + r0 * 128 + o * 16) = make_uint4(0u, 0u, 0u, 0u);
+    *reinterpret_cast<uint4*>(tile + x * Rows * 128 + r0 * 128 + o * 16) = make_uint4(0u, 0u, 0u, 0u);
   }
   tc::fence_proxy_async_smem();
   __syncwarp();

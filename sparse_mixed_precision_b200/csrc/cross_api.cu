@@ -30,17 +30,17 @@ da2_status check_cross_config(const da2_cross_config* c) {
 long q_pairs(const da2_cross_config* c) { return (c->Tq + 255) / 256; }
 
 // Parts that the keys of one query tile are split into, so that few query rows still fill the
-// processors. In units of one key tile's time: a wave of items costs its tiles plus about one for
+// processors. In units of one 128-key step's time: a wave of items costs its steps plus about one for
 // filling the pipeline and the epilogue, and joining costs about three, plus the parts' traffic.
 int choose_splits(const da2_cross_config* c) {
-  const long units = (long)c->B * c->H * q_pairs(c), tiles = ((long)c->Tk + 127) / 128;
-  if (units >= kSms || tiles < 2) return 1;
+  const long units = (long)c->B * c->H * q_pairs(c), steps = ((long)c->Tk + 127) / 128;
+  if (units >= kSms || steps < 2) return 1;
   int best = 1;
-  double best_cost = (double)(tiles + 1);
+  double best_cost = (double)(steps + 1);
   const double rows = c->Tq < 256 ? c->Tq : 256;
-  for (long s = 2; s <= tiles && s <= 64; ++s) {
+  for (long s = 2; s <= steps && s <= 64; ++s) {
     const long waves = (units * s + kSms - 1) / kSms;
-    const double cost = (double)waves * ((tiles + s - 1) / s + 1 + rows / 256.0) + 3.0;
+    const double cost = (double)waves * ((steps + s - 1) / s + 1 + rows / 256.0) + 3.0;
     if (cost < best_cost) best_cost = cost, best = (int)s;
   }
   return best;
@@ -90,15 +90,16 @@ EncodeTiled encoder() {
   return fn;
 }
 
-// Map of a strided activation [B][H][T][d] for boxes of 128 tokens x 64 channels. The stride of an
+// Map of a strided activation [B][H][T][d] for boxes of `rows` tokens x 64 channels. The stride of an
 // axis of length one is never used; the encoder wants a multiple of 16 bytes all the same.
-cudaError_t make_map(CUtensorMap* m, const da2_tensor& t, long B, long H, long T, int d, bool bf16) {
+cudaError_t make_map(CUtensorMap* m, const da2_tensor& t, long B, long H, long T, int d, bool bf16,
+                     int rows = 128) {
   const EncodeTiled fn = encoder();
   if (!fn) return cudaErrorNotSupported;
   const cuuint64_t dims[4] = {(cuuint64_t)d, (cuuint64_t)T, (cuuint64_t)H, (cuuint64_t)B};
   auto bytes = [&](int64_t s) { return (cuuint64_t)(s > 0 ? s : d) * 2; };
   const cuuint64_t strides[3] = {bytes(t.st), bytes(t.sh), bytes(t.sb)};
-  const cuuint32_t box[4] = {64, 128, 1, 1}, step[4] = {1, 1, 1, 1};
+  const cuuint32_t box[4] = {64, (cuuint32_t)rows, 1, 1}, step[4] = {1, 1, 1, 1};
   const CUresult r = fn(m, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4, t.data,
                         dims, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                         CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
@@ -124,7 +125,8 @@ da2_status common_args(const da2_cross_config* c, const da2_tensor* q, const da2
   g->kv_len = kv_len;
   g->err = static_cast<uint32_t*>(ws);
   g->stall = (c->flags & DA2_FLAG_TEST_STALL) != 0;
-  g->wait_ns = g->stall ? 50000000ull : 2000000000ull;
+  // about 2 s, longer than anything here waits; the test hook shortens it to about 50 ms
+  g->wait_clocks = g->stall ? 100000000ll : 4000000000ll;
   return DA2_OK;
 }
 
@@ -173,8 +175,9 @@ da2_status da2_cross_attention(const da2_cross_config* cfg, const da2_tensor* q,
   CrossMaps m = {};
   cudaError_t e = device_sms(&g.sms);
   if (e == cudaSuccess) e = make_map(&m.q, in[0], cfg->B, cfg->H, cfg->Tq, cfg->d, bf16);
-  if (e == cudaSuccess) e = make_map(&m.k, in[1], cfg->B, cfg->Hkv, cfg->Tk, cfg->d, bf16);
-  if (e == cudaSuccess) e = make_map(&m.v, in[2], cfg->B, cfg->Hkv, cfg->Tk, cfg->d, bf16);
+  if (e == cudaSuccess) e = make_map(&m.k, in[1], cfg->B, cfg->Hkv, cfg->Tk, cfg->d, bf16, 64);
+  if (e == cudaSuccess) e = make_map(&m.v, in[2], cfg->B, cfg->Hkv, cfg->Tk, cfg->d, bf16, 64);
+  if (e == cudaSuccess) e = make_map(&m.out, g.out, cfg->B, cfg->H, cfg->Tq, cfg->d, bf16);
   if (e == cudaSuccess) e = launch_cross_forward(g, m, bf16, stream);
   return cuda_status(e);
 }

@@ -29,12 +29,6 @@ struct Scale {
   static constexpr float kInv = kBf16 ? 1.0f : 1.0f / 64.0f;
 };
 
-// All lanes' tensor-memory accesses before, one arrival per warp after.
-__device__ __forceinline__ void warp_arrive(uint64_t* bar, int lane) {
-  tc::fence_before_sync();
-  __syncwarp();
-  if (lane == 0) tc::mbar_arrive(bar);
-}
 __device__ __forceinline__ void tmem_ld64(uint32_t taddr, uint32_t* v) {
   tc::tmem_ld32(taddr, v);
   tc::tmem_ld32(taddr + 32, v + 32);
@@ -108,7 +102,7 @@ k_cross_dq(const __grid_constant__ CrossMaps maps, const __grid_constant__ Cross
   BarsDq<D>* bars = reinterpret_cast<BarsDq<D>*>(sm + S::kBars);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int items = g.B * g.H * g.q_tiles;
-  const Guard gd{g.err, &bars->abort, g.wait_ns};
+  const Guard gd{g.err, &bars->abort, g.wait_clocks};
 
   if (tid == 0) {
     for (int s = 0; s < kStages; ++s) {
@@ -259,7 +253,7 @@ k_cross_dq(const __grid_constant__ CrossMaps maps, const __grid_constant__ Cross
     for (int i = blockIdx.x; i < items; i += gridDim.x) {
       const ItemDq w(g, i);
       if (w.nt > 0 && w.dirty(g, w.nt - 1)) {
-        if (!guard_wait(&bars->k_dirty, cleans++ & 1, gd)) break;
+        if (!warp_wait(&bars->k_dirty, cleans++ & 1, gd)) break;
         const int keys = w.keys(w.nt - 1);
         zero_rows<D>(sm + S::kStage0 + (2 * (step + w.nt - 1)) % kStages * S::kTile, keys, (keys + 15) & ~15, lane);
         if (lane == 0) tc::mbar_arrive(&bars->k_clean);
@@ -271,6 +265,7 @@ k_cross_dq(const __grid_constant__ CrossMaps maps, const __grid_constant__ Cross
     const uint32_t lane_base = tmem + ((uint32_t)((warp & 3) * 32) << 16);
     const float c = g.scale_log2;
     uint32_t step = 0, n_items = 0;
+    // no wait ends this loop early: all 256 threads must meet at the named barrier
     for (int i = blockIdx.x; i < items; i += gridDim.x) {
       const ItemDq w(g, i);
       const int row = 128 * w.qt + r;
@@ -288,7 +283,7 @@ k_cross_dq(const __grid_constant__ CrossMaps maps, const __grid_constant__ Cross
       const T* op = static_cast<const T*>(g.out.data) + w.b * g.out.sb + w.h * g.out.sh + row * g.out.st + half * (D / 2);
 #pragma unroll
       for (int k = 0; k < D / 16; ++k) o[k] = on ? __ldg(reinterpret_cast<const uint4*>(op) + k) : make_uint4(0u, 0u, 0u, 0u);
-      if (!guard_wait(&bars->q_full, n_items & 1, gd)) break;
+      guard_wait(&bars->q_full, n_items & 1, gd);
       float part = 0.0f;
 #pragma unroll
       for (int k = 0; k < D / 16; ++k) {
@@ -353,7 +348,7 @@ k_cross_dq(const __grid_constant__ CrossMaps maps, const __grid_constant__ Cross
         tc::tmem_wait_st();
         warp_arrive(&bars->ds_full[step & 1], lane);
       }
-      if (!guard_wait(&bars->dq_full, n_items & 1, gd)) break;
+      guard_wait(&bars->dq_full, n_items & 1, gd);
       tc::fence_after_sync();
       uint32_t acc[D / 2];
 #pragma unroll
@@ -447,7 +442,7 @@ k_cross_dkv(const __grid_constant__ CrossMaps maps, const __grid_constant__ Cros
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(sm_raw) + 1023) & ~uintptr_t(1023));
   BarsDkv<D>* bars = reinterpret_cast<BarsDkv<D>*>(sm + S::kBars);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const Guard gd{g.err, &bars->abort, g.wait_ns};
+  const Guard gd{g.err, &bars->abort, g.wait_clocks};
 
   if (tid == 0) {
     for (int s = 0; s < kStages; ++s) {
@@ -639,7 +634,7 @@ k_cross_dkv(const __grid_constant__ CrossMaps maps, const __grid_constant__ Cros
         warp_arrive(&bars->ds_full, lane);
       }
       // the accumulators: warps 0-3 dv, warps 4-7 dk
-      if (!guard_wait(&bars->acc_full, accs & 1, gd)) { dead = true; break; }
+      if (!warp_wait(&bars->acc_full, accs & 1, gd)) { dead = true; break; }
       tc::fence_after_sync();
       const Group w(g, gi);
       const int key = 128 * w.kt + r;

@@ -5,19 +5,20 @@
 //   more than 2^8: p then stays below 2^8, the sums are exact in the same way, and the accumulator
 //   is rescaled a few times at most.
 //
-// A work item is 256 query rows (two 128-row tiles) of one head and a run of 128-key tiles. One
-// block per processor, persistent over items; neighbouring blocks work on one head, whose keys and
-// values stay in L2. 384 threads:
-//   warps 0-3, 4-7  softmax and epilogue of tile A, B: thread r owns query row r (TMEM lane r)
-//   warp 8          issues all MMAs (one thread), owns the tensor memory
-//   warp 9          loads: Q once per item, K and V tiles through a ring of stages
-//   warp 10         zeroes value rows behind the length in the last tile, where the tensor holds
-//                   something else there (0 times NaN would reach the sum)
-// Tensor memory: S of A and B (128 columns each), O of A and B (d columns each). P overwrites its
-// own S as 16-bit pairs and is the A operand of P V, so that S of the next key tile is issued
-// directly behind P V, in order, with no buffer between; while one tile's softmax runs, the tensor
-// cores work on the other's. In the last key tile only the 16-key groups that hold a valid key are
-// multiplied.
+// A work item is 256 query rows (two 128-row tiles) of one head and a run of 64-key steps. One block
+// per processor, persistent over items; neighbouring blocks work on one head, whose keys and values
+// stay in L2. 512 threads:
+//   warps 0-3, 4-7  softmax of tile A, B: thread r owns query row r (TMEM lane r)
+//   warps 8-11      epilogue of either tile: O / sum, rounded, through shared memory to a tensor-map
+//                   store, while the softmax warps are on the next item
+//   warps 12, 13    issue the MMAs of tile A, B; warp 12 owns the tensor memory
+//   warp 14         loads K and V of the steps in turn, through a ring
+//   warp 15         loads Q, once per item (and the next item's into L2 ahead)
+// Tensor memory: per tile two S buffers of 64 columns and O (d columns). P overwrites its own S as
+// 16-bit pairs and is the A operand of P V; S of the step after next is issued directly behind P V, so
+// that a softmax warp finds its next S ready and only waits for its own arithmetic: the exponentials
+// (16 per cycle and processor) bound a step at 1024 cycles for the pair of tiles. In the last step
+// only the 16-key groups that hold a valid key are multiplied.
 #include <type_traits>
 
 #include "cross.cuh"
@@ -26,57 +27,75 @@
 namespace da2 {
 namespace {
 
-constexpr int kThreads = 384;
-constexpr int kMmaWarp = 8, kLoadWarp = 9, kCleanWarp = 10;
+constexpr int kThreads = 512;
+constexpr int kEpiWarp = 8, kMmaWarp = 12, kLoadWarp = 14, kLoadQWarp = 15;
+constexpr int kStep = 64;                                         // keys per step
 
 template <int D>
 struct Smem {
-  static constexpr uint32_t kTile = 128 * D * 2;
-  static constexpr int kStages = D == 128 ? 5 : 8;
-  static constexpr uint32_t kStage0 = 2 * kTile;
-  static constexpr uint32_t kBars = kStage0 + kStages * kTile;
-  static constexpr uint32_t kBytes = kBars + 512 + 1024;        // with room to align the base
+  static constexpr uint32_t kQ = 128 * D * 2;                     // per tile
+  static constexpr uint32_t kHalf = kStep * D * 2;
+  static constexpr uint32_t kKv = 2 * kHalf;
+  static constexpr int kStages = D == 128 ? 4 : 8;
+  static constexpr uint32_t kOut = 2 * kQ;                        // two 64-channel boxes of the epilogue
+  static constexpr uint32_t kStage0 = kOut + 2 * 16384;
+  static constexpr uint32_t kStats = kStage0 + kStages * kKv;     // [tile][row] sum and maximum
+  static constexpr uint32_t kBars = kStats + 2048;
+  static constexpr uint32_t kBytes = kBars + 512;
   static_assert(kBytes <= 232448, "shared memory budget");
 };
 template <int D>
 struct Bars {
   uint64_t kv_full[Smem<D>::kStages], kv_empty[Smem<D>::kStages];
-  uint64_t s_full[2], p_full[2], q_full[2], q_empty[2], o_full[2], o_free[2];
-  uint64_t v_dirty, v_clean, done;
+  uint64_t s_full[2][2], p_full[2][2], q_full[2], q_empty[2], pv_done[2], o_full[2], l_full[2], o_free[2];
+  uint64_t done;
   uint32_t tmem, abort;
 };
 static_assert(sizeof(Bars<64>) <= 512, "barrier area");
 
 // tensor-memory columns of tile x
-__device__ __forceinline__ constexpr uint32_t col_s(int x) { return 128u * x; }
+__device__ __forceinline__ constexpr uint32_t col_s(int x, int buf) { return 128u * x + 64u * buf; }
 __device__ __forceinline__ constexpr uint32_t col_o(int x) { return 256u + 128u * x; }
 
-// Work item i: batch entry, head, 256-row query tile, and its key tiles t0 .. t0 + nt - 1.
+// Work item i: batch entry, head, 256-row query tile, and its steps t0 .. t0 + nt - 1.
 struct Item {
   int b, h, row0, t0, nt, split, len;
   bool has_b;
   __device__ __forceinline__ Item(const CrossArgs& g, int i) {
-    split = i % g.splits;
-    i /= g.splits;
-    const int p = i % g.q_pairs;
-    i /= g.q_pairs;
-    b = i / g.H;
-    h = i - b * g.H;
-    row0 = p * 256;
+    split = 0;
+    uint32_t u = i;
+    if (g.splits > 1) {
+      split = u % g.splits;
+      u /= g.splits;
+    }
+    const uint32_t bh = u / g.q_pairs;
+    row0 = (u - bh * g.q_pairs) * 256;
+    b = bh / g.H;
+    h = bh - b * g.H;
     has_b = row0 + 128 < g.Tq;
     len = valid_keys(g, b);
-    const int tiles = (len + 127) >> 7;
-    t0 = (int)((long)tiles * split / g.splits);
-    nt = (int)((long)tiles * (split + 1) / g.splits) - t0;
+    nt = (len + kStep - 1) / kStep;
+    t0 = 0;
+    if (g.splits > 1) {
+      t0 = (int)((long)nt * split / g.splits);
+      nt = (int)((long)nt * (split + 1) / g.splits) - t0;
+    }
   }
   __device__ __forceinline__ bool has(int x) const { return x == 0 || has_b; }
-  // valid keys of this item's tile t
-  __device__ __forceinline__ int keys(int t) const { return min(128, len - 128 * (t0 + t)); }
+  // valid keys of this item's step t
+  __device__ __forceinline__ int keys(int t) const { return min(kStep, len - kStep * (t0 + t)); }
   // whether rows of the value tile must be zeroed first: the last group of 16 ends behind the length
   __device__ __forceinline__ bool dirty(const CrossArgs& g, int t) const {
     return (keys(t) & 15) != 0 && len < g.Tk;
   }
 };
+
+// The scores of a chunk from `keys` on are behind the length: -inf.
+__device__ __forceinline__ void mask32(float* s, int keys) {
+#pragma unroll
+  for (int k = 0; k < 32; ++k)
+    if (k >= keys) s[k] = -INFINITY;
+}
 
 template <int D>
 __device__ __noinline__ void rescale(uint32_t taddr, float alpha) {
@@ -94,35 +113,135 @@ __device__ __noinline__ void rescale(uint32_t taddr, float alpha) {
   tc::tmem_wait_st();
 }
 
+// Issues the MMAs of tile X. The whole warp runs this, one lane issues: every operand is the same in
+// all lanes and stays in uniform registers (issued from inside one lane's branch, an MMA took 75
+// cycles to issue, more than it runs). One warp per tile, because the waits and commits of a step take
+// most of a softmax step's time. For an item without tile B, its issuer only passes the stages on.
+template <typename T, int D, int X>
+__device__ __forceinline__ void issue(const CrossArgs& g, uint8_t* sm, Bars<D>* bars, int items, const Guard& gd,
+                                      int lane) {
+  using S = Smem<D>;
+  constexpr int kStages = S::kStages;
+  constexpr bool kBf16 = std::is_same<T, __nv_bfloat16>::value;
+  constexpr uint32_t kHi = (uint32_t)(tc::kSw128 >> 32) | (1024 >> 4);     // high word of every descriptor
+  constexpr uint32_t id_s = tc::idesc_f16(kBf16, 128, kStep, false), id_o = tc::idesc_f16(kBf16, 128, D, true);
+  const bool lead = tc::elect_one();
+  const uint32_t sm0 = tc::smem_u32(sm) >> 4;
+  // A step between its S and its P V: valid keys, and flags.
+  constexpr uint32_t kFirst = 1 << 7, kLast = 1 << 8;    // of the item
+  constexpr uint32_t kDirty = 1 << 9;                    // value rows to zero
+  constexpr uint32_t kSignal = 1 << 10;                  // P V is signalled: the next step is the last
+  constexpr uint32_t kHas = 1 << 11, kAny = 1 << 12;     // the item has this tile; not an empty step
+  uint32_t n_s = 0, n_pv = 0;                            // stages of K and of V
+  uint32_t q_items = 0, o_items = 0, own_s = 0, own_pv = 0;      // items and steps of this tile
+  auto issue_s = [&](uint32_t f) -> bool {
+    const uint32_t s = n_s % kStages, parity = (n_s / kStages) & 1;
+    ++n_s;
+    if (!(f & kHas)) return true;
+    if ((f & kFirst) && !warp_wait(&bars->q_full[X], q_items++ & 1, gd)) return false;
+    if (!warp_wait(&bars->kv_full[s], parity, gd)) return false;
+    tc::fence_after_sync();
+    const uint32_t keys = f & 127, buf = own_s++ & 1;
+    const uint32_t id = keys == kStep ? id_s : tc::idesc_f16(kBf16, 128, (keys + 15) & ~15, false);
+    const uint32_t a = (sm0 + (X * S::kQ >> 4)) | 1u << 16;
+    const uint32_t b = (sm0 + (S::kStage0 >> 4) + s * (S::kKv >> 4)) | 1u << 16;
+    if (lead) {
+#pragma unroll
+      for (int k = 0; k < D / 16; ++k)
+        tc::mma_f16(col_s(X, buf), tc::desc(a + (k / 4) * (16384 >> 4) + (k % 4) * (32 >> 4), kHi),
+                    tc::desc(b + (k / 4) * (kStep * 128 >> 4) + (k % 4) * (32 >> 4), kHi), id, k > 0);
+      tc::mma_commit(&bars->s_full[X][buf]);
+      if (f & kLast) tc::mma_commit(&bars->q_empty[X]);
+    }
+    return true;
+  };
+  auto issue_pv = [&](uint32_t f) -> bool {
+    const uint32_t s = n_pv % kStages, parity = (n_pv / kStages) & 1;
+    ++n_pv;
+    if (!(f & kHas)) {
+      if (!warp_wait(&bars->kv_full[s], parity, gd)) return false;
+      if (lead) tc::mbar_arrive(&bars->kv_empty[s]);
+      return true;
+    }
+    const uint32_t keys = f & 127, buf = own_pv & 1;
+    const uint32_t at = S::kStage0 + s * S::kKv + S::kHalf;
+    // Value rows behind the length, up to the last group of 16, may hold anything, and 0 times NaN
+    // would reach the sum: zeroed (by both issuers, with the same zeros).
+    if (f & kDirty) zero_rows<D, kStep>(sm + at, keys, (keys + 15) & ~15, lane);
+    if (!warp_wait(&bars->p_full[X][buf], (own_pv++ >> 1) & 1, gd)) return false;
+    if ((f & kFirst) && o_items++ > 0 && !warp_wait(&bars->o_free[X], o_items & 1, gd)) return false;
+    tc::fence_after_sync();
+    const uint32_t b = (sm0 + (at >> 4)) | (kStep * 128 >> 4) << 16;
+    if (lead) {
+#pragma unroll
+      for (int k = 0; k < kStep / 16; ++k)
+        if (16 * k < keys)
+          tc::mma_f16_ta(col_o(X), col_s(X, buf) + 8 * k, tc::desc(b + k * (2048 >> 4), kHi), id_o,
+                         k > 0 ? 1u : !(f & kFirst));
+      tc::mma_commit(&bars->kv_empty[s]);
+      if (f & (kLast | kSignal)) tc::mma_commit(f & kLast ? &bars->o_full[X] : &bars->pv_done[X]);
+    }
+    return true;
+  };
+  // S runs two steps ahead of P V, over the items' ends.
+  uint32_t f0 = 0, f1 = 0;
+  auto step = [&](uint32_t f) -> bool {
+    if ((f0 & kAny) && !issue_pv(f0)) return false;
+    f0 = f1;
+    f1 = f;
+    return !(f & kAny) || issue_s(f);
+  };
+  bool dead = false;
+  for (int i = blockIdx.x; i < items && !dead; i += gridDim.x) {
+    const Item w(g, i);
+    const uint32_t has = kAny | (w.has(X) ? kHas : 0u);
+    for (int t = 0; t < w.nt && !dead; ++t) {
+      uint32_t f = has | (t == 0 ? kFirst : 0u);
+      if (t == w.nt - 1) f |= kLast | (uint32_t)w.keys(t) | (w.dirty(g, t) ? kDirty : 0u);
+      else f |= kStep | (t == w.nt - 2 ? kSignal : 0u);
+      dead = !step(f);
+    }
+  }
+  dead = dead || !step(0);
+  if (!dead) step(0);
+  if (lead) tc::mma_commit(&bars->done);
+  __syncwarp();
+  guard_wait(&bars->done, 0, gd, false);           // all MMAs retired before TMEM is freed
+}
+
 template <typename T, int D>
 __global__ void __launch_bounds__(kThreads, 1)
 k_cross_forward(const __grid_constant__ CrossMaps maps, const __grid_constant__ CrossArgs g) {
   using S = Smem<D>;
   constexpr int kStages = S::kStages;
-  constexpr bool kBf16 = std::is_same<T, __nv_bfloat16>::value;
-  extern __shared__ uint8_t sm_raw[];
-  uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(sm_raw) + 1023) & ~uintptr_t(1023));
+  extern __shared__ __align__(1024) uint8_t sm[];
   Bars<D>* bars = reinterpret_cast<Bars<D>*>(sm + S::kBars);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int items = g.B * g.H * g.q_pairs * g.splits;
-  const Guard gd{g.err, &bars->abort, g.wait_ns};
+  const Guard gd{g.err, &bars->abort, g.wait_clocks};
+  if (tc::smem_u32(sm) & 1023u) {        // the swizzle needs the alignment that the declaration asks for
+    if (tid == 0) set_error(g.err, kErrBadIndex);
+    return;
+  }
 
   if (tid == 0) {
     for (int s = 0; s < kStages; ++s) {
       tc::mbar_init(&bars->kv_full[s], 1);
-      tc::mbar_init(&bars->kv_empty[s], 1);
+      tc::mbar_init(&bars->kv_empty[s], 2);              // both issuers
     }
     for (int x = 0; x < 2; ++x) {
-      tc::mbar_init(&bars->s_full[x], 1);
-      tc::mbar_init(&bars->p_full[x], 128);
+      for (int k = 0; k < 2; ++k) {
+        tc::mbar_init(&bars->s_full[x][k], 1);
+        tc::mbar_init(&bars->p_full[x][k], 4);
+      }
       tc::mbar_init(&bars->q_full[x], 1);
       tc::mbar_init(&bars->q_empty[x], 1);
+      tc::mbar_init(&bars->pv_done[x], 1);
       tc::mbar_init(&bars->o_full[x], 1);
-      tc::mbar_init(&bars->o_free[x], 128);
+      tc::mbar_init(&bars->l_full[x], 4);
+      tc::mbar_init(&bars->o_free[x], 4);
     }
-    tc::mbar_init(&bars->v_dirty, 1);
-    tc::mbar_init(&bars->v_clean, 1);
-    tc::mbar_init(&bars->done, 1);
+    tc::mbar_init(&bars->done, 2);
     bars->abort = 0u;
     tc::fence_mbar_init();
   }
@@ -133,268 +252,236 @@ k_cross_forward(const __grid_constant__ CrossMaps maps, const __grid_constant__ 
   tc::fence_before_sync();
   __syncthreads();
   tc::fence_after_sync();
-  const uint32_t tmem = bars->tmem;
+  constexpr uint32_t tmem = 0;             // all 512 columns are this block's: the base is column 0
 
-  if (warp == kLoadWarp) {
-    if (lane == 0) {
-      uint32_t n = 0, q_loads[2] = {0, 0};
-      bool dead = false;
-      auto load = [&](const CUtensorMap* map, int row, int head, int b) {
-        const uint32_t s = n % kStages;
-        if (g.stall && n == 0) { ++n; return true; }
-        if (!guard_wait(&bars->kv_empty[s], ((n / kStages) & 1) ^ 1, gd)) return false;
-        tc::mbar_arrive_expect_tx(&bars->kv_full[s], S::kTile);
-        load_tile<D>(sm + S::kStage0 + s * S::kTile, map, row, head, b, &bars->kv_full[s]);
-        ++n;
-        return true;
-      };
-      for (int i = blockIdx.x; i < items && !dead; i += gridDim.x) {
-        const Item w(g, i);
-        if (w.nt == 0) continue;
-        for (int x = 0; x < 2 && !dead; ++x) {
-          if (!w.has(x)) continue;
-          if (!guard_wait(&bars->q_empty[x], (q_loads[x] & 1) ^ 1, gd)) { dead = true; break; }
-          tc::mbar_arrive_expect_tx(&bars->q_full[x], S::kTile);
-          load_tile<D>(sm + x * S::kTile, &maps.q, w.row0 + 128 * x, w.h, w.b, &bars->q_full[x]);
-          ++q_loads[x];
-        }
-        for (int t = 0; t < w.nt && !dead; ++t) {
-          const int row = 128 * (w.t0 + t), hk = w.h / g.group;
-          dead = !load(&maps.k, row, hk, w.b);
-          if (!dead) dead = !load(&maps.v, row, hk, w.b);
-        }
-      }
-      // every copy issued above has landed before the block ends
-      for (uint32_t s = 0; s < (uint32_t)kStages && s < n; ++s)
-        guard_wait(&bars->kv_full[s], (((n - 1 - s) / kStages)) & 1, gd, false);
-      for (int x = 0; x < 2; ++x)
-        if (q_loads[x]) guard_wait(&bars->q_full[x], (q_loads[x] - 1) & 1, gd, false);
-    }
-  } else if (warp == kMmaWarp) {
-    if (lane == 0) {
-      uint32_t step = 0, q_items[2] = {0, 0}, o_items[2] = {0, 0}, p_steps[2] = {0, 0}, cleans = 0;
-      // S of tile x, key tile t of an item (global step gs)
-      auto issue_s = [&](const Item& w, int x, int t, uint32_t gs) -> bool {
-        if (t == 0 && !guard_wait(&bars->q_full[x], q_items[x]++ & 1, gd)) return false;
-        const uint32_t n = 2 * gs, s = n % kStages;
-        if (!guard_wait(&bars->kv_full[s], (n / kStages) & 1, gd)) return false;
-        tc::fence_after_sync();
-        const uint32_t id = tc::idesc_f16(kBf16, 128, (w.keys(t) + 15) & ~15, false);
-        const uint64_t a = tc::sdesc_k(sm + x * S::kTile), b = tc::sdesc_k(sm + S::kStage0 + s * S::kTile);
-#pragma unroll
-        for (int k = 0; k < D / 16; ++k) {
-          const uint64_t off = (k / 4) * (16384 >> 4) + (k % 4) * (32 >> 4);
-          tc::mma_f16(tmem + col_s(x), a + off, b + off, id, k > 0);
-        }
-        tc::mma_commit(&bars->s_full[x]);
-        if (x == 1 || !w.has_b) tc::mma_commit(&bars->kv_empty[s]);
-        if (t == w.nt - 1) tc::mma_commit(&bars->q_empty[x]);
-        return true;
-      };
-      auto issue_pv = [&](const Item& w, int x, int t, uint32_t gs) -> bool {
-        const uint32_t n = 2 * gs + 1, s = n % kStages;
-        if (!guard_wait(&bars->kv_full[s], (n / kStages) & 1, gd)) return false;
-        const bool dirty = x == 0 && w.dirty(g, t);
-        if (dirty) tc::mbar_arrive(&bars->v_dirty);      // cleaned while the softmax runs
-        if (!guard_wait(&bars->p_full[x], p_steps[x]++ & 1, gd)) return false;
-        if (dirty && !guard_wait(&bars->v_clean, cleans++ & 1, gd)) return false;
-        if (t == 0) {
-          if (o_items[x] > 0 && !guard_wait(&bars->o_free[x], (o_items[x] - 1) & 1, gd)) return false;
-          ++o_items[x];
-        }
-        tc::fence_after_sync();
-        const uint32_t id = tc::idesc_f16(kBf16, 128, D, true);
-        const uint64_t b = tc::sdesc_mn(sm + S::kStage0 + s * S::kTile, 16384);
-        const int ks = (w.keys(t) + 15) >> 4;
-#pragma unroll
-        for (int k = 0; k < 8; ++k)
-          if (k < ks)
-            tc::mma_f16_ta(tmem + col_o(x), tmem + col_s(x) + 8 * k, b + k * (2048 >> 4), id, (t > 0) | (k > 0));
-        if (x == 1 || !w.has_b) tc::mma_commit(&bars->kv_empty[s]);
-        if (t == w.nt - 1) tc::mma_commit(&bars->o_full[x]);
-        return true;
-      };
-      int i = blockIdx.x;
-      auto skip_empty = [&](int at) {
-        while (at < items && Item(g, at).nt == 0) at += gridDim.x;
-        return at;
-      };
-      bool dead = false;
-      i = skip_empty(i);
-      if (i < items) {
-        Item w(g, i);
-        for (int x = 0; x < 2 && !dead; ++x)
-          if (w.has(x)) dead = !issue_s(w, x, 0, 0);
-        while (!dead) {
-          const int in = skip_empty(i + gridDim.x);
-          const bool more = in < items;
-          const Item wn(g, more ? in : i);
-          for (int t = 0; t < w.nt && !dead; ++t, ++step) {
-            const bool last = t == w.nt - 1;
-            for (int x = 0; x < 2 && !dead; ++x) {
-              if (w.has(x)) dead = !issue_pv(w, x, t, step);
-              if (dead) break;
-              if (!last) { if (w.has(x)) dead = !issue_s(w, x, t + 1, step + 1); }
-              else if (more && wn.has(x)) dead = !issue_s(wn, x, 0, step + 1);
-            }
-          }
-          if (!more) break;
-          w = wn;
-          i = in;
-        }
-      }
-      tc::mma_commit(&bars->done);
-      guard_wait(&bars->done, 0, gd, false);       // all MMAs retired before TMEM is freed
-    }
-  } else if (warp == kCleanWarp) {
-    // The issuer names each tile to clean once it has landed: this warp, which skips all others,
-    // could not tell from the stage's own barrier which of its fills that shows.
-    uint32_t step = 0, cleans = 0;
-    for (int i = blockIdx.x; i < items; i += gridDim.x) {
-      const Item w(g, i);
-      if (w.nt > 0 && w.dirty(g, w.nt - 1)) {
-        if (!guard_wait(&bars->v_dirty, cleans++ & 1, gd)) break;
-        const int keys = w.keys(w.nt - 1);
-        zero_rows<D>(sm + S::kStage0 + (2 * (step + w.nt - 1) + 1) % kStages * S::kTile, keys, (keys + 15) & ~15, lane);
-        if (lane == 0) tc::mbar_arrive(&bars->v_clean);
-      }
-      step += w.nt;
-    }
-  } else if (warp < kMmaWarp) {
+  // registers: 2 x 152 + 2 x 104 = 4 x 128, the launch's
+  if (warp < kEpiWarp) {
     const int x = warp >> 2, r = tid & 127;
     const uint32_t lane_base = tmem + ((uint32_t)((warp & 3) * 32) << 16);
-    const uint32_t tS = lane_base + col_s(x), tO = lane_base + col_o(x);
+    const uint32_t tO = lane_base + col_o(x);
     const float c = g.scale_log2;
-    uint32_t step = 0, done_items = 0;
+    float2* stats = reinterpret_cast<float2*>(sm + S::kStats) + 128 * x + r;
+    uint32_t step = 0, n_items = 0, signals = 0;
     for (int i = blockIdx.x; i < items; i += gridDim.x) {
       const Item w(g, i);
-      if (!w.has(x)) continue;
-      const int row = w.row0 + 128 * x + r;
-      const bool on = row < g.Tq;
-      const size_t flat = ((size_t)w.b * g.H + w.h) * g.Tq + row;       // row of lse and the parts
-      const size_t part = (size_t)w.split * g.B * g.H * g.Tq + flat;
+      if (!w.has(x) || w.nt == 0) continue;
       float m = -INFINITY, l = 0.0f;
       for (int t = 0; t < w.nt; ++t, ++step) {
-        guard_wait(&bars->s_full[x], step & 1, gd);
+        const uint32_t buf = step & 1, tS = lane_base + col_s(x, buf);
+        guard_wait(&bars->s_full[x][buf], (step >> 1) & 1, gd);
         tc::fence_after_sync();
         const int keys = w.keys(t);
-        uint32_t su[128];
-        float* s = reinterpret_cast<float*>(su);
+        // The row is read twice, 32 columns at a time in rolled loops: the maximum, then the
+        // exponentials. Unrolled with the row in registers, the loop's code does not fit the
+        // instruction cache beside the other warps' and waits for instructions (2.3 of 9 stalled
+        // cycles per instruction).
+        const int chunks = (keys + 31) >> 5;
+        float mx = -INFINITY;
+#pragma unroll 1
+        for (int k0 = 0; k0 < keys; k0 += 32) {
+          uint32_t u[32];
+          float* s = reinterpret_cast<float*>(u);
+          tc::tmem_ld32(tS + k0, u);
+          tc::tmem_wait_ld16(u);
+          tc::tmem_wait_ld16(u + 16);
+          if (k0 + 32 > keys) mask32(s, keys - k0);
+          float m4[4];
 #pragma unroll
-        for (int k = 0; k < 128; k += 32)
-          if (k < keys) tc::tmem_ld32(tS + k, su + k);
+          for (int q = 0; q < 4; ++q) m4[q] = max3(s[q], s[4 + q], s[8 + q]);
 #pragma unroll
-        for (int k = 0; k < 128; k += 16) tc::tmem_wait_ld16(su + k);
-        if (keys < 128) {
+          for (int q = 0; q < 4; ++q) m4[q] = max3(m4[q], s[12 + q], s[16 + q]);
 #pragma unroll
-          for (int k = 0; k < 128; ++k)
-            if (k >= keys) s[k] = -INFINITY;
+          for (int q = 0; q < 4; ++q) m4[q] = max3(m4[q], s[20 + q], s[24 + q]);
+          mx = max3(mx, max3(m4[0], m4[1], s[28]), max3(max3(m4[2], m4[3], s[29]), s[30], s[31]));
         }
-        float mx[4];
-#pragma unroll
-        for (int q = 0; q < 4; ++q) mx[q] = s[q];
-#pragma unroll
-        for (int k = 4; k < 128; k += 8) {
-#pragma unroll
-          for (int q = 0; q < 4; ++q) mx[q] = k + 4 + q < 128 ? max3(mx[q], s[k + q], s[k + 4 + q]) : fmaxf(mx[q], s[k + q]);
-        }
-        const float m_new = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c;
+        const float m_new = mx * c;
         if (t == 0) {
           m = m_new;
         } else {
           const bool grow = m_new > m + 8.0f;
           if (__any_sync(0xffffffffu, grow)) {
             const float alpha = grow ? ex2(m - m_new) : 1.0f;
-            rescale<D>(tO, alpha);                       // the previous P V is done: S came behind it
+            // the previous step's P V is done: S of the next step was issued behind it, or, at the
+            // item's end, it has a barrier of its own
+            if (t < w.nt - 1) guard_wait(&bars->s_full[x][buf ^ 1], ((step + 1) >> 1) & 1, gd);
+            else guard_wait(&bars->pv_done[x], signals & 1, gd);
+            tc::fence_after_sync();
+            rescale<D>(tO, alpha);
             l *= alpha;
             if (grow) m = m_new;
           }
         }
         const float bias = m == -INFINITY ? 0.0f : -m;   // a row of -inf scores so far: p = 0
         const f32x2 c2 = pk2(c, c), b2 = pk2(bias, bias);
-        f32x2 sum[2] = {pk2(0.0f, 0.0f), pk2(0.0f, 0.0f)};
+        f32x2 sum[2] = {pk2(l, 0.0f), pk2(0.0f, 0.0f)};
+#pragma unroll 1
+        for (int i = 0; i < chunks; ++i) {
+          uint32_t u[32], p[16];
+          float* s = reinterpret_cast<float*>(u);
+          tc::tmem_ld32(tS + 32 * i, u);
+          tc::tmem_wait_ld16(u);
+          tc::tmem_wait_ld16(u + 16);
+          if (32 * i + 32 > keys) mask32(s, keys - 32 * i);
 #pragma unroll
-        for (int k0 = 0; k0 < 128; k0 += 32) {
-          if (k0 < keys) {
-            uint32_t p[16];
-#pragma unroll
-            for (int k = 0; k < 32; k += 2) {
-              float a, b;
-              upk2(fma2(pk2(s[k0 + k], s[k0 + k + 1]), c2, b2), a, b);
-              a = ex2(a);
-              b = ex2(b);
-              sum[(k >> 1) & 1] = add2(sum[(k >> 1) & 1], pk2(a, b));
-              p[k >> 1] = pack16<T>(a, b);
-            }
-            tc::tmem_st16(tS + k0 / 2, p);
+          for (int k = 0; k < 32; k += 2) {
+            float a, b;
+            upk2(fma2(pk2(s[k], s[k + 1]), c2, b2), a, b);
+            a = ex2(a);
+            b = ex2(b);
+            sum[(k >> 1) & 1] = add2(sum[(k >> 1) & 1], pk2(a, b));
+            p[k >> 1] = pack16<T>(a, b);
           }
+          tc::tmem_st16(tS + 16 * i, p);                 // over columns that have been read
         }
         float a0, a1, b0, b1;
         upk2(sum[0], a0, a1);
         upk2(sum[1], b0, b1);
-        l += (a0 + a1) + (b0 + b1);
+        l = (a0 + a1) + (b0 + b1);
         tc::tmem_wait_st();
-        tc::fence_before_sync();
-        tc::mbar_arrive(&bars->p_full[x]);
+        warp_arrive(&bars->p_full[x][buf], lane);
       }
-      if (w.nt == 0) {                                   // no key: zero, and no weight in a join
-        if (on && g.splits > 1) {
-          float4* o = reinterpret_cast<float4*>(g.part_o + part * D);
-          for (int k = 0; k < D / 4; ++k) o[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-          g.part_lse[part] = -INFINITY;
-        } else if (on) {
-          uint4* o = reinterpret_cast<uint4*>(static_cast<T*>(g.out.data) + w.b * g.out.sb + w.h * g.out.sh +
-                                              row * g.out.st);
-          for (int k = 0; k < D / 8; ++k) o[k] = make_uint4(0u, 0u, 0u, 0u);
-          if (g.lse) g.lse[flat] = -INFINITY;
+      // the epilogue has taken the previous item's statistics
+      if (n_items > 0 && !warp_wait(&bars->o_free[x], (n_items - 1) & 1, gd)) break;
+      signals += w.nt > 1;
+      *stats = make_float2(l, m);
+      warp_arrive(&bars->l_full[x], lane);
+      ++n_items;
+    }
+  } else {
+  if (warp == kLoadWarp) {
+    if (lane == 0) {
+      uint32_t n = 0;
+      bool dead = false;
+      for (int i = blockIdx.x; i < items && !dead; i += gridDim.x) {
+        const Item w(g, i);
+        for (int t = 0; t < w.nt; ++t, ++n) {
+          const uint32_t s = n % kStages;
+          if (g.stall && n == 0) continue;
+          if (!guard_wait(&bars->kv_empty[s], ((n / kStages) & 1) ^ 1, gd)) { dead = true; break; }
+          tc::mbar_arrive_expect_tx(&bars->kv_full[s], S::kKv);
+          load_tile<D, kStep>(sm + S::kStage0 + s * S::kKv, &maps.k, kStep * (w.t0 + t), w.h / g.group, w.b, &bars->kv_full[s]);
+          load_tile<D, kStep>(sm + S::kStage0 + s * S::kKv+S::kHalf, &maps.v, kStep * (w.t0 + t), w.h / g.group, w.b, &bars->kv_full[s]);
         }
-        continue;
       }
-      if (!guard_wait(&bars->o_full[x], done_items++ & 1, gd)) break;
-      tc::fence_after_sync();
-      const float inv = 1.0f / l;
-      const float lse2 = m + log2f(l);
+      // every copy issued above has landed before the block ends
+      for (uint32_t s = 0; s < (uint32_t)kStages && s < n; ++s)
+        guard_wait(&bars->kv_full[s], (((n - 1 - s) / kStages)) & 1, gd, false);
+    }
+  } else if (warp == kLoadQWarp) {
+    if (lane == 0) {
+      uint32_t q_loads[2] = {0, 0};
+      bool dead = false;
+      for (int i = blockIdx.x; i < items && !dead; i += gridDim.x) {
+        const Item w(g, i);
+        if (w.nt == 0) continue;
 #pragma unroll
-      for (int k0 = 0; k0 < D; k0 += 32) {
-        uint32_t v[32];
-        tc::tmem_ld32(tO + k0, v);
-        tc::tmem_wait_ld16(v);
-        tc::tmem_wait_ld16(v + 16);
-        if (k0 + 32 == D) {                              // O is free once the last column is read
-          tc::fence_before_sync();
-          tc::mbar_arrive(&bars->o_free[x]);
+        for (int x = 0; x < 2; ++x) {
+          if (dead || !w.has(x)) continue;
+          if (!guard_wait(&bars->q_empty[x], (q_loads[x] & 1) ^ 1, gd)) { dead = true; continue; }
+          tc::mbar_arrive_expect_tx(&bars->q_full[x], S::kQ);
+          load_tile<D>(sm + x * S::kQ, &maps.q, w.row0 + 128 * x, w.h, w.b, &bars->q_full[x]);
+          ++q_loads[x];
         }
-        if (!on) continue;
-        if (g.splits > 1) {
-          float4* o = reinterpret_cast<float4*>(g.part_o + part * D + k0);
+        if (i + (int)gridDim.x < items) {
+          const Item wn(g, i + gridDim.x);
+          for (int x = 0; x < 2; ++x)
+            if (wn.has(x))
+              for (int c = 0; c < D; c += 64) tc::tma_prefetch_4d(&maps.q, c, wn.row0 + 128 * x, wn.h, wn.b);
+        }
+      }
 #pragma unroll
-          for (int k = 0; k < 8; ++k)
-            o[k] = make_float4(__uint_as_float(v[4 * k]) * inv, __uint_as_float(v[4 * k + 1]) * inv,
-                               __uint_as_float(v[4 * k + 2]) * inv, __uint_as_float(v[4 * k + 3]) * inv);
-        } else {
-          uint4* o = reinterpret_cast<uint4*>(static_cast<T*>(g.out.data) + w.b * g.out.sb + w.h * g.out.sh +
-                                              row * g.out.st + k0);
+      for (int x = 0; x < 2; ++x)
+        if (q_loads[x]) guard_wait(&bars->q_full[x], (q_loads[x] - 1) & 1, gd, false);
+    }
+  } else if (warp == kMmaWarp) {
+    issue<T, D, 0>(g, sm, bars, items, gd, lane);
+  } else if (warp == kMmaWarp + 1) {
+    issue<T, D, 1>(g, sm, bars, items, gd, lane);
+  } else if (warp < kMmaWarp) {
+    // No wait ends this loop early: all 128 threads must meet at the named barrier. After an abort
+    // every wait returns at once and what is written is undefined.
+    const int r = tid & 127;
+    const bool lead = tid == kEpiWarp * 32;
+    const uint32_t lane_base = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+    uint32_t n_items[2] = {0, 0}, boxes = 0;
+    for (int i = blockIdx.x; i < items; i += gridDim.x) {
+      const Item w(g, i);
+      for (int x = 0; x < 2; ++x) {
+        if (!w.has(x)) continue;
+        const int row = w.row0 + 128 * x + r;
+        const bool on = row < g.Tq;
+        const size_t flat = ((size_t)w.b * g.H + w.h) * g.Tq + row;     // row of lse and the parts
+        const size_t part = (size_t)w.split * g.B * g.H * g.Tq + flat;
+        if (w.nt == 0) {                                 // no key: zero, and no weight in a join
+          if (on && g.splits > 1) {
+            float4* o = reinterpret_cast<float4*>(g.part_o + part * D);
+            for (int k = 0; k < D / 4; ++k) o[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+            g.part_lse[part] = -INFINITY;
+          } else if (on) {
+            uint4* o = reinterpret_cast<uint4*>(static_cast<T*>(g.out.data) + w.b * g.out.sb + w.h * g.out.sh +
+                                                row * g.out.st);
+            for (int k = 0; k < D / 8; ++k) o[k] = make_uint4(0u, 0u, 0u, 0u);
+            if (g.lse) g.lse[flat] = -INFINITY;
+          }
+          continue;
+        }
+        guard_wait(&bars->l_full[x], n_items[x] & 1, gd);
+        const float2 lm = reinterpret_cast<const float2*>(sm + S::kStats)[128 * x + r];
+        guard_wait(&bars->o_full[x], n_items[x] & 1, gd);
+        ++n_items[x];
+        tc::fence_after_sync();
+        const float inv = 1.0f / lm.x;
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
+        for (int c0 = 0; c0 < D; c0 += 64) {
+          uint32_t v[64];
+          tc::tmem_ld32(lane_base + col_o(x) + c0, v);
+          tc::tmem_ld32(lane_base + col_o(x) + c0 + 32, v + 32);
+#pragma unroll
+          for (int k = 0; k < 64; k += 16) tc::tmem_wait_ld16(v + k);
+          if (c0 + 64 == D) warp_arrive(&bars->o_free[x], lane);        // statistics and O are read
+          if (g.splits > 1) {
+            if (on) {
+              float4* o = reinterpret_cast<float4*>(g.part_o + part * D + c0);
+#pragma unroll
+              for (int k = 0; k < 16; ++k)
+                o[k] = make_float4(__uint_as_float(v[4 * k]) * inv, __uint_as_float(v[4 * k + 1]) * inv,
+                                   __uint_as_float(v[4 * k + 2]) * inv, __uint_as_float(v[4 * k + 3]) * inv);
+            }
+            continue;
+          }
+          uint8_t* box = sm + S::kOut + (boxes++ & 1) * 16384;
+          if (lead) tc::bulk_wait_read<1>();             // the store before last has read this box
+          asm volatile("bar.sync 2, 128;" ::: "memory");
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
             uint32_t u[4];
 #pragma unroll
             for (int e = 0; e < 4; ++e)
               u[e] = pack16<T>(__uint_as_float(v[8 * k + 2 * e]) * inv, __uint_as_float(v[8 * k + 2 * e + 1]) * inv);
-            o[k] = make_uint4(u[0], u[1], u[2], u[3]);
+            *reinterpret_cast<uint4*>(box + r * 128 + ((k ^ (r & 7)) << 4)) = make_uint4(u[0], u[1], u[2], u[3]);
+          }
+          tc::fence_proxy_async_smem();
+          asm volatile("bar.sync 2, 128;" ::: "memory");
+          if (lead) {
+            tc::tma_store_4d(&maps.out, box, c0, w.row0 + 128 * x, w.h, w.b);
+            tc::bulk_commit();
           }
         }
-      }
-      if (on) {
-        if (g.splits > 1) g.part_lse[part] = lse2;
-        else if (g.lse) g.lse[flat] = lse2 * kLn2;
+        if (on) {
+          const float lse2 = lm.y + log2f(lm.x);
+          if (g.splits > 1) g.part_lse[part] = lse2;
+          else if (g.lse) g.lse[flat] = lse2 * kLn2;
+        }
       }
     }
+    if (lead) tc::bulk_wait_all();
+  }
   }
   tc::fence_before_sync();
   __syncthreads();
   if (warp == kMmaWarp) {
     tc::fence_after_sync();
-    tc::tmem_dealloc(tmem, 512);
+    tc::tmem_dealloc(bars->tmem, 512);
   }
 }
 
