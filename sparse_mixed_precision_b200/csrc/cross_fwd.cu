@@ -6,8 +6,9 @@
 //   is rescaled a few times at most.
 //
 // A work item is 256 query rows (two 128-row tiles) of one head and a run of 64-key steps. One block
-// per processor, persistent over items; neighbouring blocks work on one head, whose keys and values
-// stay in L2. 512 threads:
+// per processor, persistent over items. Neighbouring blocks work on one head, whose keys and values
+// stay in L2; or, in token-major tensors, on the heads of the same tokens, whose rows are neighbours in
+// memory, while the keys and values of all heads fit L2. 512 threads:
 //   warps 0-3, 4-7  softmax of tile A, B: thread r owns query row r (TMEM lane r)
 //   warps 8-11      epilogue of either tile: O / sum, rounded, through shared memory to a tensor-map
 //                   store, while the softmax warps are on the next item
@@ -62,24 +63,37 @@ struct Item {
   int b, h, row0, t0, nt, split, len;
   bool has_b;
   __device__ __forceinline__ Item(const CrossArgs& g, int i) {
-    split = 0;
+    int v[7];
+    decode(g, i, v);
+    b = v[0], h = v[1], row0 = v[2], t0 = v[3], nt = v[4], split = v[5], len = v[6];
+    has_b = row0 + 128 < g.Tq;
+  }
+  // not inline: its divisions in each of the kernel's roles would crowd the instruction cache
+  static __device__ __noinline__ void decode(const CrossArgs& g, int i, int* v) {
+    int b, h, row0, t0 = 0, split = 0;
     uint32_t u = i;
     if (g.splits > 1) {
       split = u % g.splits;
       u /= g.splits;
     }
-    const uint32_t bh = u / g.q_pairs;
-    row0 = (u - bh * g.q_pairs) * 256;
-    b = bh / g.H;
-    h = bh - b * g.H;
-    has_b = row0 + 128 < g.Tq;
-    len = valid_keys(g, b);
-    nt = (len + kStep - 1) / kStep;
-    t0 = 0;
+    if (g.heads_first) {
+      const uint32_t bp = u / g.H;
+      h = u - bp * g.H;
+      b = bp / g.q_pairs;
+      row0 = (bp - b * g.q_pairs) * 256;
+    } else {
+      const uint32_t bh = u / g.q_pairs;
+      row0 = (u - bh * g.q_pairs) * 256;
+      b = bh / g.H;
+      h = bh - b * g.H;
+    }
+    const int len = valid_keys(g, b);
+    int nt = (len + kStep - 1) / kStep;
     if (g.splits > 1) {
       t0 = (int)((long)nt * split / g.splits);
       nt = (int)((long)nt * (split + 1) / g.splits) - t0;
     }
+    v[0] = b, v[1] = h, v[2] = row0, v[3] = t0, v[4] = nt, v[5] = split, v[6] = len;
   }
   __device__ __forceinline__ bool has(int x) const { return x == 0 || has_b; }
   // valid keys of this item's step t
@@ -191,19 +205,25 @@ __device__ __forceinline__ void issue(const CrossArgs& g, uint8_t* sm, Bars<D>* 
     f1 = f;
     return !(f & kAny) || issue_s(f);
   };
-  bool dead = false;
-  for (int i = blockIdx.x; i < items && !dead; i += gridDim.x) {
-    const Item w(g, i);
-    const uint32_t has = kAny | (w.has(X) ? kHas : 0u);
-    for (int t = 0; t < w.nt && !dead; ++t) {
-      uint32_t f = has | (t == 0 ? kFirst : 0u);
+  int i = blockIdx.x, t = 0, tail = 2;                   // behind the last item two empty steps
+  Item w(g, min(i, items - 1));
+  while (true) {
+    while (i < items && t >= w.nt) {
+      i += gridDim.x;
+      t = 0;
+      if (i < items) w = Item(g, i);
+    }
+    uint32_t f = 0;
+    if (i < items) {
+      f = kAny | (w.has(X) ? kHas : 0u) | (t == 0 ? kFirst : 0u);
       if (t == w.nt - 1) f |= kLast | (uint32_t)w.keys(t) | (w.dirty(g, t) ? kDirty : 0u);
       else f |= kStep | (t == w.nt - 2 ? kSignal : 0u);
-      dead = !step(f);
+      ++t;
+    } else if (tail-- == 0) {
+      break;
     }
+    if (!step(f)) break;
   }
-  dead = dead || !step(0);
-  if (!dead) step(0);
   if (lead) tc::mma_commit(&bars->done);
   __syncwarp();
   guard_wait(&bars->done, 0, gd, false);           // all MMAs retired before TMEM is freed
@@ -225,6 +245,7 @@ k_cross_forward(const __grid_constant__ CrossMaps maps, const __grid_constant__ 
   }
 
   if (tid == 0) {
+#pragma unroll 1
     for (int s = 0; s < kStages; ++s) {
       tc::mbar_init(&bars->kv_full[s], 1);
       tc::mbar_init(&bars->kv_empty[s], 2);              // both issuers
@@ -364,6 +385,7 @@ k_cross_forward(const __grid_constant__ CrossMaps maps, const __grid_constant__ 
         }
       }
       // every copy issued above has landed before the block ends
+#pragma unroll 1
       for (uint32_t s = 0; s < (uint32_t)kStages && s < n; ++s)
         guard_wait(&bars->kv_full[s], (((n - 1 - s) / kStages)) & 1, gd, false);
     }
@@ -403,7 +425,7 @@ k_cross_forward(const __grid_constant__ CrossMaps maps, const __grid_constant__ 
     const int r = tid & 127;
     const bool lead = tid == kEpiWarp * 32;
     const uint32_t lane_base = tmem + ((uint32_t)((warp & 3) * 32) << 16);
-    uint32_t n_items[2] = {0, 0}, boxes = 0;
+    uint32_t n_items[2] = {0, 0}, tiles = 0;
     for (int i = blockIdx.x; i < items; i += gridDim.x) {
       const Item w(g, i);
       for (int x = 0; x < 2; ++x) {
@@ -415,55 +437,63 @@ k_cross_forward(const __grid_constant__ CrossMaps maps, const __grid_constant__ 
         if (w.nt == 0) {                                 // no key: zero, and no weight in a join
           if (on && g.splits > 1) {
             float4* o = reinterpret_cast<float4*>(g.part_o + part * D);
+#pragma unroll 1
             for (int k = 0; k < D / 4; ++k) o[k] = make_float4(0.f, 0.f, 0.f, 0.f);
             g.part_lse[part] = -INFINITY;
           } else if (on) {
             uint4* o = reinterpret_cast<uint4*>(static_cast<T*>(g.out.data) + w.b * g.out.sb + w.h * g.out.sh +
                                                 row * g.out.st);
+#pragma unroll 1
             for (int k = 0; k < D / 8; ++k) o[k] = make_uint4(0u, 0u, 0u, 0u);
             if (g.lse) g.lse[flat] = -INFINITY;
           }
           continue;
         }
+        // the boxes of this tile, once the stores of their last use have read them
+        uint8_t* box = sm + S::kOut + (D == 64 ? (tiles & 1) * 16384 : 0);
+        if (lead) tc::bulk_wait_read<D == 64 ? 1 : 0>();
+        asm volatile("bar.sync 2, 128;" ::: "memory");
         guard_wait(&bars->l_full[x], n_items[x] & 1, gd);
         const float2 lm = reinterpret_cast<const float2*>(sm + S::kStats)[128 * x + r];
         guard_wait(&bars->o_full[x], n_items[x] & 1, gd);
         ++n_items[x];
+        ++tiles;
         tc::fence_after_sync();
         const float inv = 1.0f / lm.x;
-#pragma unroll
-        for (int c0 = 0; c0 < D; c0 += 64) {
-          uint32_t v[64];
+#pragma unroll 1
+        for (int c0 = 0; c0 < D; c0 += 32) {
+          uint32_t v[32];
           tc::tmem_ld32(lane_base + col_o(x) + c0, v);
-          tc::tmem_ld32(lane_base + col_o(x) + c0 + 32, v + 32);
-#pragma unroll
-          for (int k = 0; k < 64; k += 16) tc::tmem_wait_ld16(v + k);
-          if (c0 + 64 == D) warp_arrive(&bars->o_free[x], lane);        // statistics and O are read
+          tc::tmem_wait_ld16(v);
+          tc::tmem_wait_ld16(v + 16);
+          if (c0 + 32 == D) warp_arrive(&bars->o_free[x], lane);        // statistics and O are read
           if (g.splits > 1) {
             if (on) {
               float4* o = reinterpret_cast<float4*>(g.part_o + part * D + c0);
 #pragma unroll
-              for (int k = 0; k < 16; ++k)
+              for (int k = 0; k < 8; ++k)
                 o[k] = make_float4(__uint_as_float(v[4 * k]) * inv, __uint_as_float(v[4 * k + 1]) * inv,
                                    __uint_as_float(v[4 * k + 2]) * inv, __uint_as_float(v[4 * k + 3]) * inv);
             }
             continue;
           }
-          uint8_t* box = sm + S::kOut + (boxes++ & 1) * 16384;
-          if (lead) tc::bulk_wait_read<1>();             // the store before last has read this box
-          asm volatile("bar.sync 2, 128;" ::: "memory");
+          uint8_t* at = box + (c0 >> 6) * 16384 + r * 128;
 #pragma unroll
-          for (int k = 0; k < 8; ++k) {
+          for (int k = 0; k < 4; ++k) {
             uint32_t u[4];
 #pragma unroll
             for (int e = 0; e < 4; ++e)
               u[e] = pack16<T>(__uint_as_float(v[8 * k + 2 * e]) * inv, __uint_as_float(v[8 * k + 2 * e + 1]) * inv);
-            *reinterpret_cast<uint4*>(box + r * 128 + ((k ^ (r & 7)) << 4)) = make_uint4(u[0], u[1], u[2], u[3]);
+            *reinterpret_cast<uint4*>(at + (((k + (c0 >> 3)) ^ r) & 7) * 16) = make_uint4(u[0], u[1], u[2], u[3]);
           }
+        }
+        if (g.splits == 1) {
           tc::fence_proxy_async_smem();
           asm volatile("bar.sync 2, 128;" ::: "memory");
           if (lead) {
-            tc::tma_store_4d(&maps.out, box, c0, w.row0 + 128 * x, w.h, w.b);
+#pragma unroll
+            for (int c0 = 0; c0 < D; c0 += 64)
+              tc::tma_store_4d(&maps.out, box + (c0 >> 6) * 16384, c0, w.row0 + 128 * x, w.h, w.b);
             tc::bulk_commit();
           }
         }
