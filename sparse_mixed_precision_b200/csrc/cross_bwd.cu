@@ -20,7 +20,7 @@ namespace da2 {
 namespace {
 
 constexpr int kThreads = 384;
-constexpr int kMmaWarp = 8, kLoadWarp = 9, kCleanWarp = 10;
+constexpr int kMmaWarp = 8, kLoadWarp = 11;             // warps 8 to 10 issue MMAs
 
 template <typename T>
 struct Scale {
@@ -68,7 +68,7 @@ template <int D>
 struct BarsDq {
   uint64_t kv_full[SmemDq<D>::kStages], kv_empty[SmemDq<D>::kStages];
   uint64_t q_full, q_empty, s_full, s_free, dp_full, dp_free, ds_full[2], ds_free[2], dq_full, dq_free;
-  uint64_t k_dirty, k_clean, done;
+  uint64_t done;
   uint32_t tmem, abort;
 };
 static_assert(sizeof(BarsDq<64>) <= 384, "barrier area");
@@ -78,18 +78,45 @@ constexpr uint32_t kDqS = 0, kDqP = 128, kDqAcc = 256, kDqDs = 384;   // columns
 struct ItemDq {
   int b, h, qt, nt, len;
   __device__ __forceinline__ ItemDq(const CrossArgs& g, int i) {
-    qt = i % g.q_tiles;
-    i /= g.q_tiles;
-    b = i / g.H;
-    h = i - b * g.H;
-    len = valid_keys(g, b);
-    nt = (len + 127) >> 7;
+    int v[5];
+    decode(g, i, v);
+    b = v[0], h = v[1], qt = v[2], nt = v[3], len = v[4];
+  }
+  // not inline: its divisions in each of the kernel's roles would crowd the instruction cache
+  static __device__ __noinline__ void decode(const CrossArgs& g, uint32_t u, int* v) {
+    int b, h, qt;
+    if (g.heads_first) {
+      const uint32_t bp = u / g.H;
+      h = u - bp * g.H;
+      b = bp / g.q_tiles;
+      qt = bp - b * g.q_tiles;
+    } else {
+      const uint32_t bh = u / g.q_tiles;
+      qt = u - bh * g.q_tiles;
+      b = bh / g.H;
+      h = bh - b * g.H;
+    }
+    const int len = valid_keys(g, b);
+    v[0] = b, v[1] = h, v[2] = qt, v[3] = (len + 127) >> 7, v[4] = len;
   }
   __device__ __forceinline__ int keys(int t) const { return min(128, len - 128 * t); }
   __device__ __forceinline__ bool dirty(const CrossArgs& g, int t) const {
     return (keys(t) & 15) != 0 && len < g.Tk;
   }
 };
+
+// The S and dP products, each A (128 rows) x 128 rows of a tile over d channels, and the accumulating
+// product of a 16-bit operand in tensor memory with a tile read by columns. Executed by one lane; the
+// operands are the same in all lanes of the issuing warp and stay in uniform registers.
+constexpr uint32_t kDescHi = (uint32_t)(tc::kSw128 >> 32) | (1024 >> 4);
+template <int D>
+__device__ __forceinline__ void mma_rows(uint32_t acc, uint32_t a, uint32_t b, uint32_t id) {
+#pragma unroll
+  for (int k = 0; k < D / 16; ++k) {
+    const uint32_t off = (k / 4) * (16384 >> 4) + (k % 4) * (32 >> 4);
+    tc::mma_f16(acc, tc::desc((a + off) | 1u << 16, kDescHi), tc::desc((b + off) | 1u << 16, kDescHi), id, k > 0);
+  }
+}
 
 template <typename T, int D>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -110,7 +137,7 @@ k_cross_dq(const __grid_constant__ CrossMaps maps, const __grid_constant__ Cross
       tc::mbar_init(&bars->kv_empty[s], 1);
     }
     tc::mbar_init(&bars->q_full, 1);
-    tc::mbar_init(&bars->q_empty, 1 + 8);                // the MMAs, and the warps that read dout
+    tc::mbar_init(&bars->q_empty, 2 + 8);                // S and dP, and the warps that read dout
     tc::mbar_init(&bars->s_full, 1);
     tc::mbar_init(&bars->s_free, 8);
     tc::mbar_init(&bars->dp_full, 1);
@@ -121,9 +148,7 @@ k_cross_dq(const __grid_constant__ CrossMaps maps, const __grid_constant__ Cross
     }
     tc::mbar_init(&bars->dq_full, 1);
     tc::mbar_init(&bars->dq_free, 8);
-    tc::mbar_init(&bars->k_dirty, 1);
-    tc::mbar_init(&bars->k_clean, 1);
-    tc::mbar_init(&bars->done, 1);
+    tc::mbar_init(&bars->done, 3);
     bars->abort = 0u;
     tc::fence_mbar_init();
   }
@@ -134,7 +159,7 @@ k_cross_dq(const __grid_constant__ CrossMaps maps, const __grid_constant__ Cross
   tc::fence_before_sync();
   __syncthreads();
   tc::fence_after_sync();
-  const uint32_t tmem = bars->tmem;
+  constexpr uint32_t tmem = 0;             // all 512 columns are this block's: the base is column 0
 
   if (warp == kLoadWarp) {
     if (lane == 0) {
@@ -162,104 +187,72 @@ k_cross_dq(const __grid_constant__ CrossMaps maps, const __grid_constant__ Cross
           if (!dead) dead = !load(&maps.v, 128 * t, w.h / g.group, w.b);
         }
       }
+#pragma unroll 1
       for (uint32_t s = 0; s < (uint32_t)kStages && s < n; ++s)
         guard_wait(&bars->kv_full[s], ((n - 1 - s) / kStages) & 1, gd, false);
       if (q_loads) guard_wait(&bars->q_full, (q_loads - 1) & 1, gd, false);
     }
-  } else if (warp == kMmaWarp) {
-    if (lane == 0) {
-      uint32_t step = 0, q_items = 0, acc_items = 0, cleans = 0;
-      const uint64_t dQ = tc::sdesc_k(sm), dDo = tc::sdesc_k(sm + S::kDo);
-      auto wait_stage = [&](uint32_t n) { return guard_wait(&bars->kv_full[n % kStages], (n / kStages) & 1, gd); };
-      auto product = [&](uint32_t acc, uint64_t a, const uint8_t* tile, int keys) {
-        const uint32_t id = tc::idesc_f16(kBf16, 128, (keys + 15) & ~15, false);
-        const uint64_t b = tc::sdesc_k(tile);
-#pragma unroll
-        for (int k = 0; k < D / 16; ++k) {
-          const uint64_t off = (k / 4) * (16384 >> 4) + (k % 4) * (32 >> 4);
-          tc::mma_f16(tmem + acc, a + off, b + off, id, k > 0);
-        }
-      };
-      auto issue_s = [&](const ItemDq& w, int t, uint32_t gs) -> bool {
-        if (gs > 0 && !guard_wait(&bars->s_free, (gs - 1) & 1, gd)) return false;
-        if (t == 0 && !guard_wait(&bars->q_full, q_items++ & 1, gd)) return false;
-        if (!wait_stage(2 * gs)) return false;
-        tc::fence_after_sync();
-        product(kDqS, dQ, sm + S::kStage0 + (2 * gs) % kStages * S::kTile, w.keys(t));
-        tc::mma_commit(&bars->s_full);
-        return true;
-      };
-      auto issue_dp = [&](const ItemDq& w, int t, uint32_t gs) -> bool {
-        if (gs > 0 && !guard_wait(&bars->dp_free, (gs - 1) & 1, gd)) return false;
-        const uint32_t n = 2 * gs + 1;
-        if (!wait_stage(n)) return false;
-        tc::fence_after_sync();
-        product(kDqP, dDo, sm + S::kStage0 + n % kStages * S::kTile, w.keys(t));
-        tc::mma_commit(&bars->dp_full);
-        tc::mma_commit(&bars->kv_empty[n % kStages]);
-        if (t == w.nt - 1) tc::mma_commit(&bars->q_empty);
-        return true;
-      };
-      auto issue_dq = [&](const ItemDq& w, int t, uint32_t gs) -> bool {
-        if (w.dirty(g, t)) tc::mbar_arrive(&bars->k_dirty);      // landed long ago: S has read it
-        if (!guard_wait(&bars->ds_full[gs & 1], (gs >> 1) & 1, gd)) return false;
-        if (w.dirty(g, t) && !guard_wait(&bars->k_clean, cleans++ & 1, gd)) return false;
-        if (t == 0) {
-          if (acc_items > 0 && !guard_wait(&bars->dq_free, (acc_items - 1) & 1, gd)) return false;
-          ++acc_items;
-        }
-        tc::fence_after_sync();
-        const uint32_t s = (2 * gs) % kStages, id = tc::idesc_f16(kBf16, 128, D, true);
-        const uint64_t b = tc::sdesc_mn(sm + S::kStage0 + s * S::kTile, 16384);
-        const int ks = (w.keys(t) + 15) >> 4;
-#pragma unroll
-        for (int k = 0; k < 8; ++k)
-          if (k < ks)
-            tc::mma_f16_ta(tmem + kDqAcc, tmem + kDqDs + 64 * (gs & 1) + 8 * k, b + k * (2048 >> 4), id,
-                           (t > 0) | (k > 0));
-        tc::mma_commit(&bars->kv_empty[s]);
-        tc::mma_commit(&bars->ds_free[gs & 1]);
-        if (t == w.nt - 1) tc::mma_commit(&bars->dq_full);
-        return true;
-      };
-      auto skip_empty = [&](int at) {
-        while (at < items && ItemDq(g, at).nt == 0) at += gridDim.x;
-        return at;
-      };
-      int i = skip_empty(blockIdx.x);
-      if (i < items) {
-        ItemDq w(g, i);
-        bool dead = !issue_s(w, 0, 0) || !issue_dp(w, 0, 0);
-        while (!dead) {
-          const int in = skip_empty(i + gridDim.x);
-          const bool more = in < items;
-          const ItemDq wn(g, more ? in : i);
-          for (int t = 0; t < w.nt && !dead; ++t, ++step) {
-            const bool last = t == w.nt - 1;
-            if (!last) dead = !issue_s(w, t + 1, step + 1) || !issue_dp(w, t + 1, step + 1);
-            else if (more) dead = !issue_s(wn, 0, step + 1) || !issue_dp(wn, 0, step + 1);
-            if (!dead) dead = !issue_dq(w, t, step);
-          }
-          if (!more) break;
-          w = wn;
-          i = in;
-        }
-      }
-      tc::mma_commit(&bars->done);
-      guard_wait(&bars->done, 0, gd, false);
-    }
-  } else if (warp == kCleanWarp) {
-    uint32_t step = 0, cleans = 0;
-    for (int i = blockIdx.x; i < items; i += gridDim.x) {
+  } else if (warp >= kMmaWarp) {
+    // Three issuing warps, one per product: a warp's waits stand behind the MMAs it has issued, so that
+    // one warp for all three adds their times to its own. The whole warp runs the loop, one lane issues.
+    const int role = warp - kMmaWarp;      // 0: S, 1: dP, 2: dq
+    const bool lead = tc::elect_one();
+    const uint32_t sm0 = tc::smem_u32(sm) >> 4, stage0 = sm0 + (S::kStage0 >> 4);
+    uint32_t step = 0, n_items = 0;
+    bool dead = false;
+    for (int i = blockIdx.x; i < items && !dead; i += gridDim.x) {
       const ItemDq w(g, i);
-      if (w.nt > 0 && w.dirty(g, w.nt - 1)) {
-        if (!warp_wait(&bars->k_dirty, cleans++ & 1, gd)) break;
-        const int keys = w.keys(w.nt - 1);
-        zero_rows<D>(sm + S::kStage0 + (2 * (step + w.nt - 1)) % kStages * S::kTile, keys, (keys + 15) & ~15, lane);
-        if (lane == 0) tc::mbar_arrive(&bars->k_clean);
+      for (int t = 0; t < w.nt && !dead; ++t, ++step) {
+        const uint32_t n = 2 * step + (role == 1 ? 1 : 0), s = n % kStages, tile = stage0 + s * (S::kTile >> 4);
+        const int keys = w.keys(t);
+        const bool last = t == w.nt - 1;
+        dead = !warp_wait(&bars->kv_full[s], (n / kStages) & 1, gd);
+        if (role < 2) {
+          if (t == 0) dead = dead || !warp_wait(&bars->q_full, n_items & 1, gd);
+          if (step > 0) dead = dead || !warp_wait(role ? &bars->dp_free : &bars->s_free, (step - 1) & 1, gd);
+          if (dead) break;
+          tc::fence_after_sync();
+          const uint32_t id = tc::idesc_f16(kBf16, 128, (keys + 15) & ~15, false);
+          if (lead) {
+            if (role == 0) {
+              mma_rows<D>(tmem + kDqS, sm0, tile, id);
+              tc::mma_commit(&bars->s_full);
+            } else {
+              mma_rows<D>(tmem + kDqP, sm0 + (S::kDo >> 4), tile, id);
+              tc::mma_commit(&bars->dp_full);
+              tc::mma_commit(&bars->kv_empty[s]);
+            }
+            if (last) tc::mma_commit(&bars->q_empty);
+          }
+        } else {
+          // Key rows behind the length, up to the last group of 16, may hold anything, and 0 times NaN
+          // would reach the sum: zeroed (S, which may be reading them, masks its columns).
+          if (last && w.dirty(g, t)) zero_rows<D>(sm + S::kStage0 + s * S::kTile, keys, (keys + 15) & ~15, lane);
+          const uint32_t buf = step & 1;
+          dead = dead || !warp_wait(&bars->ds_full[buf], (step >> 1) & 1, gd);
+          if (t == 0 && n_items > 0) dead = dead || !warp_wait(&bars->dq_free, (n_items - 1) & 1, gd);
+          if (dead) break;
+          tc::fence_after_sync();
+          const uint32_t b = tile | (16384 >> 4) << 16;
+          constexpr uint32_t id = tc::idesc_f16(kBf16, 128, D, true);
+          if (lead) {
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+              if (16 * k < keys)
+                tc::mma_f16_ta(tmem + kDqAcc, tmem + kDqDs + 64 * buf + 8 * k, tc::desc(b + k * (2048 >> 4), kDescHi),
+                               id, k > 0 ? 1u : t > 0);
+            tc::mma_commit(&bars->kv_empty[s]);
+            tc::mma_commit(&bars->ds_free[buf]);
+            if (last) tc::mma_commit(&bars->dq_full);
+          }
+        }
+        __syncwarp();
       }
-      step += w.nt;
+      n_items += w.nt > 0;
     }
+    if (lead) tc::mma_commit(&bars->done);
+    __syncwarp();
+    guard_wait(&bars->done, 0, gd, false);           // all issuers' MMAs retired before TMEM is freed
   } else if (warp < kMmaWarp) {
     const int half = warp >> 2, r = tid & 127;
     const uint32_t lane_base = tmem + ((uint32_t)((warp & 3) * 32) << 16);
@@ -335,10 +328,16 @@ k_cross_dq(const __grid_constant__ CrossMaps maps, const __grid_constant__ Cross
         for (int k = 0; k < 64; k += 2) {
           float x, y;
           upk2(mul2(add2(pk2(p[k], p[k + 1]), d2), pk2(s[k], s[k + 1])), x, y);
-          if (k >= keys) x = 0.0f;                       // also NaN from behind the length
-          if (k + 1 >= keys) y = 0.0f;
-          ds[k >> 1] = pack16<T>(x, y);
+          p[k] = x;
+          p[k + 1] = y;
         }
+        if (keys < 64) {                                 // also NaN from behind the length
+#pragma unroll
+          for (int k = 0; k < 64; ++k)
+            if (k >= keys) p[k] = 0.0f;
+        }
+#pragma unroll
+        for (int k = 0; k < 32; ++k) ds[k] = pack16<T>(p[2 * k], p[2 * k + 1]);
         if (step >= 2) {
           guard_wait(&bars->ds_free[step & 1], ((step >> 1) - 1) & 1, gd);
           tc::fence_after_sync();
@@ -367,7 +366,7 @@ k_cross_dq(const __grid_constant__ CrossMaps maps, const __grid_constant__ Cross
   __syncthreads();
   if (warp == kMmaWarp) {
     tc::fence_after_sync();
-    tc::tmem_dealloc(tmem, 512);
+    tc::tmem_dealloc(bars->tmem, 512);
   }
 }
 
@@ -447,17 +446,17 @@ k_cross_dkv(const __grid_constant__ CrossMaps maps, const __grid_constant__ Cros
   if (tid == 0) {
     for (int s = 0; s < kStages; ++s) {
       tc::mbar_init(&bars->q_full[s], 1);
-      tc::mbar_init(&bars->q_empty[s], 1);
+      tc::mbar_init(&bars->q_empty[s], s & 1 ? 2 : 1);   // Q: dk; dout: dP and dv
     }
     tc::mbar_init(&bars->kv_full, 1);
-    tc::mbar_init(&bars->kv_empty, 1);
+    tc::mbar_init(&bars->kv_empty, 2);
     tc::mbar_init(&bars->s_full, 1);
     tc::mbar_init(&bars->p_full, 8);
     tc::mbar_init(&bars->dp_full, 1);
     tc::mbar_init(&bars->ds_full, 8);
-    tc::mbar_init(&bars->acc_full, 1);
+    tc::mbar_init(&bars->acc_full, 2);
     tc::mbar_init(&bars->acc_free, 8);
-    tc::mbar_init(&bars->done, 1);
+    tc::mbar_init(&bars->done, 2);
     bars->abort = 0u;
     tc::fence_mbar_init();
   }
@@ -468,7 +467,7 @@ k_cross_dkv(const __grid_constant__ CrossMaps maps, const __grid_constant__ Cros
   tc::fence_before_sync();
   __syncthreads();
   tc::fence_after_sync();
-  const uint32_t tmem = bars->tmem;
+  constexpr uint32_t tmem = 0;             // all 512 columns are this block's: the base is column 0
   const Share sh(g);
   const long u0 = sh.begin(blockIdx.x), u1 = sh.begin(blockIdx.x + 1);
 
@@ -505,75 +504,78 @@ k_cross_dkv(const __grid_constant__ CrossMaps maps, const __grid_constant__ Cros
         }
         u = gi * sh.n + e;
       }
+#pragma unroll 1
       for (uint32_t s = 0; s < (uint32_t)kStages && s < n; ++s)
         guard_wait(&bars->q_full[s], ((n - 1 - s) / kStages) & 1, gd, false);
       if (groups) guard_wait(&bars->kv_full, (groups - 1) & 1, gd, false);
     }
-  } else if (warp == kMmaWarp) {
-    if (lane == 0 && u0 < u1) {
+  } else if (warp == kMmaWarp || warp == kMmaWarp + 1) {
+    if (u0 < u1) {
+      // Two issuing warps: S and dv, dP and dk, each next S (dP) behind the dv (dk) whose operand it
+      // overwrites. The whole warp runs the loop, one lane issues.
+      const int y = warp - kMmaWarp;
+      const bool lead = tc::elect_one();
+      const uint32_t sm0 = (tc::smem_u32(sm) + (y ? S::kV : 0)) >> 4, stage0 = (tc::smem_u32(sm) + S::kStage0) >> 4;
+      constexpr uint32_t id_s = tc::idesc_f16(kBf16, 128, 128, false), id_o = tc::idesc_f16(kBf16, 128, D, true);
       uint32_t groups = 0, accs = 0;
-      const uint64_t dK = tc::sdesc_k(sm), dV = tc::sdesc_k(sm + S::kV);
-      const uint32_t id_s = tc::idesc_f16(kBf16, 128, 128, false), id_o = tc::idesc_f16(kBf16, 128, D, true);
-      auto tile = [&](uint32_t n) { return sm + S::kStage0 + n % kStages * S::kTile; };
-      auto wait_stage = [&](uint32_t n) { return guard_wait(&bars->q_full[n % kStages], (n / kStages) & 1, gd); };
-      auto product = [&](uint32_t acc, uint64_t a, const uint8_t* t) {
-        const uint64_t b = tc::sdesc_k(t);
-#pragma unroll
-        for (int k = 0; k < D / 16; ++k) {
-          const uint64_t off = (k / 4) * (16384 >> 4) + (k % 4) * (32 >> 4);
-          tc::mma_f16(tmem + acc, a + off, b + off, id_s, k > 0);
+      uint64_t* const made = y ? &bars->dp_full : &bars->s_full;
+      uint64_t* const ready = y ? &bars->ds_full : &bars->p_full;
+      // S (of Q, even stages) or dP (of dout, odd stages) of a step
+      auto rows = [&](bool new_group, bool last_of_group, uint32_t gs) -> bool {
+        const uint32_t n = 2 * gs + y, s = n % kStages;
+        if (new_group && !warp_wait(&bars->kv_full, groups++ & 1, gd)) return false;
+        if (!warp_wait(&bars->q_full[s], (n / kStages) & 1, gd)) return false;
+        tc::fence_after_sync();
+        if (lead) {
+          if (y) mma_rows<D>(tmem + kKvP, sm0, stage0 + s * (S::kTile >> 4), id_s);
+          else mma_rows<D>(tmem + kKvS, sm0, stage0 + s * (S::kTile >> 4), id_s);
+          tc::mma_commit(made);
+          if (y) tc::mma_commit(&bars->q_empty[s]);      // dout; its other use is dv
+          if (last_of_group) tc::mma_commit(&bars->kv_empty);
         }
-      };
-      // acc += A^T tile, A the 16-bit operand in the two 32-column halves behind col and col + 64
-      auto accumulate = [&](uint32_t acc, uint32_t col, const uint8_t* t, bool first) {
-        const uint64_t b = tc::sdesc_mn(t, 16384);
-#pragma unroll
-        for (int k = 0; k < 8; ++k)
-          tc::mma_f16_ta(tmem + acc, tmem + col + 64 * (k >> 2) + 8 * (k & 3), b + k * (2048 >> 4), id_o,
-                         !first | (k > 0));
-      };
-      auto issue_s = [&](bool new_group, uint32_t gs) -> bool {
-        if (new_group && !guard_wait(&bars->kv_full, groups++ & 1, gd)) return false;
-        if (!wait_stage(2 * gs)) return false;
-        tc::fence_after_sync();
-        product(kKvS, dK, tile(2 * gs));
-        tc::mma_commit(&bars->s_full);
+        __syncwarp();
         return true;
       };
-      auto issue_dp = [&](bool last_of_group, uint32_t gs) -> bool {
-        if (!wait_stage(2 * gs + 1)) return false;
-        tc::fence_after_sync();
-        product(kKvP, dV, tile(2 * gs + 1));
-        tc::mma_commit(&bars->dp_full);
-        if (last_of_group) tc::mma_commit(&bars->kv_empty);
-        return true;
-      };
-      // unit u is the last of its run within a group
-      auto ends = [&](long u) { return u + 1 == u1 || (u + 1) % sh.n == 0; };
-      bool dead = !issue_s(true, 0) || !issue_dp(ends(u0), 0);
+      // runs of units within a group: what is left of this run, and of the next unit's
+      const int n = sh.n;
+      int left = (int)min((long)(n - u0 % n), u1 - u0);
+      bool dead = !rows(true, left == 1, 0);
       bool first = true;
       uint32_t step = 0;
-      for (long u = u0; u < u1 && !dead; ++u, ++step) {
-        const bool last = ends(u), more = u + 1 < u1;
-        if (!guard_wait(&bars->p_full, step & 1, gd)) break;
-        if (first && accs > 0 && !guard_wait(&bars->acc_free, (accs - 1) & 1, gd)) break;
+      for (long todo = u1 - u0; todo > 0 && !dead; --todo, ++step) {
+        const bool last = left == 1, more = todo > 1;
+        const int left1 = last ? (int)min((long)n, todo - 1) : left - 1;
+        const uint32_t at = 2 * step + 1 - y, s = at % kStages;          // dout for dv, Q for dk
+        if (!warp_wait(ready, step & 1, gd)) break;
+        if (first && accs > 0 && !warp_wait(&bars->acc_free, (accs - 1) & 1, gd)) break;
+        if (!warp_wait(&bars->q_full[s], (at / kStages) & 1, gd)) break;
         tc::fence_after_sync();
-        accumulate(kKvDv, kKvS, tile(2 * step + 1), first);
-        tc::mma_commit(&bars->q_empty[(2 * step + 1) % kStages]);
-        if (more && !issue_s(last, step + 1)) break;
-        if (!guard_wait(&bars->ds_full, step & 1, gd)) break;
-        tc::fence_after_sync();
-        accumulate(kKvDk, kKvP, tile(2 * step), first);
-        tc::mma_commit(&bars->q_empty[(2 * step) % kStages]);
-        if (last) {
-          tc::mma_commit(&bars->acc_full);
-          ++accs;
+        const uint32_t b = (stage0 + s * (S::kTile >> 4)) | (16384 >> 4) << 16;
+        if (lead) {
+          // the 16-bit operand lies in the two 32-column halves behind column 0 and 64 of its region
+          if (y) {
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+              tc::mma_f16_ta(tmem + kKvDk, tmem + kKvP + 64 * (k >> 2) + 8 * (k & 3), tc::desc(b + k * (2048 >> 4), kDescHi),
+                             id_o, k > 0 ? 1u : !first);
+          } else {
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+              tc::mma_f16_ta(tmem + kKvDv, tmem + kKvS + 64 * (k >> 2) + 8 * (k & 3), tc::desc(b + k * (2048 >> 4), kDescHi),
+                             id_o, k > 0 ? 1u : !first);
+          }
+          tc::mma_commit(&bars->q_empty[s]);
+          if (last) tc::mma_commit(&bars->acc_full);
         }
-        if (more && !issue_dp(ends(u + 1), step + 1)) break;
+        __syncwarp();
+        accs += last;
+        if (more && !rows(last, left1 == 1, step + 1)) break;
         first = last;
+        left = left1;
       }
-      tc::mma_commit(&bars->done);
-      guard_wait(&bars->done, 0, gd, false);
+      if (lead) tc::mma_commit(&bars->done);
+      __syncwarp();
+      guard_wait(&bars->done, 0, gd, false);         // both issuers' MMAs retired before TMEM is freed
     }
   } else if (warp < kMmaWarp) {
     const int half = warp >> 2, r = tid & 127;
@@ -666,7 +668,7 @@ k_cross_dkv(const __grid_constant__ CrossMaps maps, const __grid_constant__ Cros
   __syncthreads();
   if (warp == kMmaWarp) {
     tc::fence_after_sync();
-    tc::tmem_dealloc(tmem, 512);
+    tc::tmem_dealloc(bars->tmem, 512);
   }
 }
 
