@@ -59,17 +59,26 @@ SIGNATURES = {
 }
 
 
-def _dtypes():
-    import torch
-    return {torch.bfloat16: 0, torch.float16: 1}
+_torch = None                       # imported with the first call, like everywhere in the package
+_DTYPES = {}                        # DA2_DTYPE_* -> torch dtype
+
+
+def _load():
+    global _torch
+    if _torch is None:
+        import torch
+        _DTYPES.update({0: torch.bfloat16, 1: torch.float16})
+        _torch = torch
+    return _torch
 
 
 def _dtype_code(dtype):
-    import torch
+    torch = _load()
     dtype = torch.bfloat16 if dtype is None else dtype
-    if dtype not in _dtypes():
-        raise ValueError(f"dtype must be bfloat16 or float16, not {dtype}")
-    return _dtypes()[dtype]
+    for code, d in _DTYPES.items():
+        if d == dtype:
+            return code
+    raise ValueError(f"dtype must be bfloat16 or float16, not {dtype}")
 
 
 def _with_layout(cfg, layout):
@@ -100,72 +109,72 @@ class _Args:
     """Checks a call's tensors (the C ABI sees bare pointers) and turns them into its arguments.
     Every device tensor must sit on the device of the stream the call runs on."""
 
+    __slots__ = ("fn", "cfg", "dtype", "bthd", "stream", "index")
+
     def __init__(self, fn, cfg, stream):
-        import torch
-        self.fn, self.cfg, self.torch, self._given = fn, cfg, torch, stream
+        torch = _load()
+        self.fn, self.cfg, self.bthd = fn, cfg, cfg.layout == "bthd"
+        self.dtype = _DTYPES.get(cfg.dtype)
+        if stream is None and torch.cuda.is_initialized():
+            stream = torch.cuda.current_stream()
+        self.stream = stream
+        self.index = -2 if stream is None else stream.device_index
 
-    @property
-    def stream(self):
-        if self._given is None:
-            self._given = self.torch.cuda.current_stream()
-        return self._given
-
-    def _device(self, name, t):
-        if not isinstance(t, self.torch.Tensor):
+    def _refuse(self, name, t, dtype, shape):
+        """The error of a tensor that a check has turned down."""
+        if not isinstance(t, _torch.Tensor):
             raise TypeError(f"{self.fn}: {name} must be a torch.Tensor")
+        if t.dtype != dtype and dtype is not None:
+            raise ValueError(f"{self.fn}: {name} has dtype {t.dtype}; the call needs {dtype}")
+        if shape is not None and tuple(t.shape) != tuple(shape):
+            raise ValueError(f"{self.fn}: {name} has shape {tuple(t.shape)}; the call needs {tuple(shape)}")
         if t.device.type != "cuda":
             raise ValueError(f"{self.fn}: {name} must be a CUDA tensor, not on {t.device}")
-        if t.device != self.stream.device:
-            raise ValueError(f"{self.fn}: {name} is on {t.device} but the call runs on {self.stream.device}")
+        raise ValueError(f"{self.fn}: {name} is on {t.device} but the call runs on "
+                         f"{'no device' if self.stream is None else self.stream.device}")
 
     def act(self, name, t, H, T):
         """A strided activation of H heads and T tokens."""
         cfg = self.cfg
-        if not isinstance(t, self.torch.Tensor):
-            raise TypeError(f"{self.fn}: {name} must be a torch.Tensor")
-        if _dtypes().get(t.dtype) != cfg.dtype:
-            raise ValueError(f"{self.fn}: {name} has dtype {t.dtype}; the configuration needs "
-                             f"{[d for d, c in _dtypes().items() if c == cfg.dtype][0]}")
-        bthd = cfg.layout == "bthd"
-        want = (cfg.B, T, H, cfg.d) if bthd else (cfg.B, H, T, cfg.d)
-        if tuple(t.shape) != want:
-            raise ValueError(f"{self.fn}: {name} has shape {tuple(t.shape)}; the configuration needs {want}")
-        if t.stride(3) != 1:
+        want = (cfg.B, T, H, cfg.d) if self.bthd else (cfg.B, H, T, cfg.d)
+        if not (isinstance(t, _torch.Tensor) and t.dtype is self.dtype and t.shape == want):
+            self._refuse(name, t, self.dtype, want)
+        sb, s1, s2, sc = t.stride()
+        if sc != 1:
             raise ValueError(f"{self.fn}: {name} must have contiguous channels")
-        self._device(name, t)
-        sh, st = (t.stride(2), t.stride(1)) if bthd else (t.stride(1), t.stride(2))
-        return ctypes.byref(Tensor(t.data_ptr(), t.stride(0), sh, st))
+        if t.get_device() != self.index:
+            self._refuse(name, t, self.dtype, want)
+        return Tensor(t.data_ptr(), sb, s2, s1) if self.bthd else Tensor(t.data_ptr(), sb, s1, s2)
 
     def plain(self, name, t, dtype, shape):
-        """A contiguous tensor of one shape, or None."""
+        """The address of a contiguous tensor of one shape, or None."""
         if t is None:
             return None
-        if not isinstance(t, self.torch.Tensor):
-            raise TypeError(f"{self.fn}: {name} must be a torch.Tensor")
-        if t.dtype != dtype:
-            raise ValueError(f"{self.fn}: {name} must be {dtype}, not {t.dtype}")
-        if tuple(t.shape) != tuple(shape):
-            raise ValueError(f"{self.fn}: {name} has shape {tuple(t.shape)}; the call needs {tuple(shape)}")
+        if not (isinstance(t, _torch.Tensor) and t.dtype is dtype and t.shape == shape):
+            self._refuse(name, t, dtype, shape)
         if not t.is_contiguous():
             raise ValueError(f"{self.fn}: {name} must be contiguous")
-        self._device(name, t)
-        return ctypes.c_void_p(t.data_ptr())
+        if t.get_device() != self.index:
+            self._refuse(name, t, dtype, shape)
+        return t.data_ptr()
 
     def buffer(self, name, t):
-        """A contiguous byte buffer: (pointer, size)."""
-        if not isinstance(t, self.torch.Tensor):
-            raise TypeError(f"{self.fn}: {name} must be a torch.Tensor")
+        """A contiguous byte buffer: (address, size)."""
+        if not isinstance(t, _torch.Tensor):
+            self._refuse(name, t, None, None)
         if not t.is_contiguous():
             raise ValueError(f"{self.fn}: {name} must be contiguous")
-        self._device(name, t)
-        return ctypes.c_void_p(t.data_ptr()), t.numel() * t.element_size()
+        if t.get_device() != self.index:
+            self._refuse(name, t, None, None)
+        return t.data_ptr(), t.nbytes
 
     def call(self, *args):
-        device = self.stream.device
-        here = self.torch.cuda.current_device() == device.index
-        with contextlib.nullcontext() if here else self.torch.cuda.device(device):
-            st = getattr(_pkg.lib(), self.fn)(ctypes.byref(self.cfg), *args, ctypes.c_void_p(self.stream.cuda_stream))
-        _pkg._check(self.fn, st)
+        cuda = _torch.cuda
+        here = cuda.current_device() == self.index
+        with contextlib.nullcontext() if here else cuda.device(self.index):
+            st = getattr(_pkg.lib(), self.fn)(self.cfg, *args, self.stream.cuda_stream)
+        if st:
+            _pkg._check(self.fn, st)
 
 
 def _size(fn, cfg):
@@ -175,7 +184,7 @@ def _size(fn, cfg):
 
 
 def _norm_args(a, cfg, wq, wk, cos, sin):
-    f32 = a.torch.float32
+    f32 = _torch.float32
     table = (cfg.T_rot, cfg.d // 2) if not cfg.flags & ROPE_BATCHED else (cfg.B, cfg.T_rot, cfg.d // 2)
     if cfg.T_rot > 0 and (cos is None or sin is None):
         raise ValueError(f"{a.fn}: cos and sin are needed to rotate {cfg.T_rot} tokens")
@@ -212,7 +221,7 @@ def qk_norm_rope_backward(cfg, dq_out, dk_out, q, k, wq, wk, cos, sin, dq, dk, d
     """Gradients of qk_norm_rope: dq, dk (of q, k) and dwq, dwk (float32 [d], or None) from
     dq_out, dk_out (of its outputs) and its inputs. dq may be dq_out or q, dk may be dk_out or k."""
     a = _Args("da2_qk_norm_rope_backward", cfg, stream)
-    f32 = a.torch.float32
+    f32 = _torch.float32
     dw = a.plain("dwq", dwq, f32, (cfg.d,)), a.plain("dwk", dwk, f32, (cfg.d,))
     a.call(a.act("dq_out", dq_out, cfg.Hq, cfg.T), _key_act(a, cfg, "dk_out", dk_out),
            a.act("q", q, cfg.Hq, cfg.T), _key_act(a, cfg, "k", k), *_norm_args(a, cfg, wq, wk, cos, sin),
@@ -233,8 +242,8 @@ def cross_attention_workspace(cfg, device, backward=False):
 
 
 def _cross_args(a, cfg, lse, kv_len):
-    return (a.plain("lse", lse, a.torch.float32, (cfg.B, cfg.H, cfg.Tq)),
-            a.plain("kv_len", kv_len, a.torch.int32, (cfg.B,)))
+    return (a.plain("lse", lse, _torch.float32, (cfg.B, cfg.H, cfg.Tq)),
+            a.plain("kv_len", kv_len, _torch.int32, (cfg.B,)))
 
 
 def cross_attention(cfg, q, k, v, out, ws, kv_len=None, lse=None, stream=None):

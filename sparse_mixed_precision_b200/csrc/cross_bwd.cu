@@ -20,7 +20,7 @@ namespace da2 {
 namespace {
 
 constexpr int kThreads = 384;
-constexpr int kMmaWarp = 8, kLoadWarp = 11;             // warps 8 to 10 issue MMAs
+constexpr int kMmaWarp = 8, kLoadWarp = 11;             // warps 8 to 10 issue MMAs (dq), warp 8 (dk, dv)
 
 template <typename T>
 struct Scale {
@@ -446,17 +446,17 @@ k_cross_dkv(const __grid_constant__ CrossMaps maps, const __grid_constant__ Cros
   if (tid == 0) {
     for (int s = 0; s < kStages; ++s) {
       tc::mbar_init(&bars->q_full[s], 1);
-      tc::mbar_init(&bars->q_empty[s], s & 1 ? 2 : 1);   // Q: dk; dout: dP and dv
+      tc::mbar_init(&bars->q_empty[s], 1);
     }
     tc::mbar_init(&bars->kv_full, 1);
-    tc::mbar_init(&bars->kv_empty, 2);
+    tc::mbar_init(&bars->kv_empty, 1);
     tc::mbar_init(&bars->s_full, 1);
     tc::mbar_init(&bars->p_full, 8);
     tc::mbar_init(&bars->dp_full, 1);
     tc::mbar_init(&bars->ds_full, 8);
-    tc::mbar_init(&bars->acc_full, 2);
+    tc::mbar_init(&bars->acc_full, 1);
     tc::mbar_init(&bars->acc_free, 8);
-    tc::mbar_init(&bars->done, 2);
+    tc::mbar_init(&bars->done, 1);
     bars->abort = 0u;
     tc::fence_mbar_init();
   }
@@ -509,73 +509,80 @@ k_cross_dkv(const __grid_constant__ CrossMaps maps, const __grid_constant__ Cros
         guard_wait(&bars->q_full[s], ((n - 1 - s) / kStages) & 1, gd, false);
       if (groups) guard_wait(&bars->kv_full, (groups - 1) & 1, gd, false);
     }
-  } else if (warp == kMmaWarp || warp == kMmaWarp + 1) {
+  } else if (warp == kMmaWarp) {
     if (u0 < u1) {
-      // Two issuing warps: S and dv, dP and dk, each next S (dP) behind the dv (dk) whose operand it
-      // overwrites. The whole warp runs the loop, one lane issues.
-      const int y = warp - kMmaWarp;
+      // the whole warp runs this, one lane issues
       const bool lead = tc::elect_one();
-      const uint32_t sm0 = (tc::smem_u32(sm) + (y ? S::kV : 0)) >> 4, stage0 = (tc::smem_u32(sm) + S::kStage0) >> 4;
+      const uint32_t sm0 = tc::smem_u32(sm) >> 4, stage0 = sm0 + (S::kStage0 >> 4);
       constexpr uint32_t id_s = tc::idesc_f16(kBf16, 128, 128, false), id_o = tc::idesc_f16(kBf16, 128, D, true);
       uint32_t groups = 0, accs = 0;
-      uint64_t* const made = y ? &bars->dp_full : &bars->s_full;
-      uint64_t* const ready = y ? &bars->ds_full : &bars->p_full;
-      // S (of Q, even stages) or dP (of dout, odd stages) of a step
-      auto rows = [&](bool new_group, bool last_of_group, uint32_t gs) -> bool {
-        const uint32_t n = 2 * gs + y, s = n % kStages;
+      // acc += A^T tile, A the 16-bit operand in the two 32-column halves behind col and col + 64
+      auto accumulate = [&](uint32_t acc, uint32_t col, uint32_t stage, bool first) {
+        const uint32_t b = (stage0 + stage * (S::kTile >> 4)) | (16384 >> 4) << 16;
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+          tc::mma_f16_ta(tmem + acc, tmem + col + 64 * (k >> 2) + 8 * (k & 3), tc::desc(b + k * (2048 >> 4), kDescHi),
+                         id_o, k > 0 ? 1u : !first);
+      };
+      auto issue_s = [&](bool new_group, uint32_t gs) -> bool {
         if (new_group && !warp_wait(&bars->kv_full, groups++ & 1, gd)) return false;
+        const uint32_t s = 2 * gs % kStages;
+        if (!warp_wait(&bars->q_full[s], (2 * gs / kStages) & 1, gd)) return false;
+        tc::fence_after_sync();
+        if (lead) {
+          mma_rows<D>(tmem + kKvS, sm0, stage0 + s * (S::kTile >> 4), id_s);
+          tc::mma_commit(&bars->s_full);
+        }
+        __syncwarp();
+        return true;
+      };
+      auto issue_dp = [&](bool last_of_group, uint32_t gs) -> bool {
+        const uint32_t n = 2 * gs + 1, s = n % kStages;
         if (!warp_wait(&bars->q_full[s], (n / kStages) & 1, gd)) return false;
         tc::fence_after_sync();
         if (lead) {
-          if (y) mma_rows<D>(tmem + kKvP, sm0, stage0 + s * (S::kTile >> 4), id_s);
-          else mma_rows<D>(tmem + kKvS, sm0, stage0 + s * (S::kTile >> 4), id_s);
-          tc::mma_commit(made);
-          if (y) tc::mma_commit(&bars->q_empty[s]);      // dout; its other use is dv
+          mma_rows<D>(tmem + kKvP, sm0 + (S::kV >> 4), stage0 + s * (S::kTile >> 4), id_s);
+          tc::mma_commit(&bars->dp_full);
           if (last_of_group) tc::mma_commit(&bars->kv_empty);
         }
         __syncwarp();
         return true;
       };
-      // runs of units within a group: what is left of this run, and of the next unit's
+      // runs of units within a group: what is left of this run and the next
       const int n = sh.n;
       int left = (int)min((long)(n - u0 % n), u1 - u0);
-      bool dead = !rows(true, left == 1, 0);
+      bool dead = !issue_s(true, 0) || !issue_dp(left == 1, 0);
       bool first = true;
       uint32_t step = 0;
       for (long todo = u1 - u0; todo > 0 && !dead; --todo, ++step) {
         const bool last = left == 1, more = todo > 1;
-        const int left1 = last ? (int)min((long)n, todo - 1) : left - 1;
-        const uint32_t at = 2 * step + 1 - y, s = at % kStages;          // dout for dv, Q for dk
-        if (!warp_wait(ready, step & 1, gd)) break;
-        if (first && accs > 0 && !warp_wait(&bars->acc_free, (accs - 1) & 1, gd)) break;
-        if (!warp_wait(&bars->q_full[s], (at / kStages) & 1, gd)) break;
+        const int left1 = last ? (int)min((long)n, todo - 1) : left - 1;      // of the next unit's run
+        dead = !warp_wait(&bars->p_full, step & 1, gd);
+        if (!dead && first && accs > 0) dead = !warp_wait(&bars->acc_free, (accs - 1) & 1, gd);
+        if (dead) break;
         tc::fence_after_sync();
-        const uint32_t b = (stage0 + s * (S::kTile >> 4)) | (16384 >> 4) << 16;
         if (lead) {
-          // the 16-bit operand lies in the two 32-column halves behind column 0 and 64 of its region
-          if (y) {
-#pragma unroll
-            for (int k = 0; k < 8; ++k)
-              tc::mma_f16_ta(tmem + kKvDk, tmem + kKvP + 64 * (k >> 2) + 8 * (k & 3), tc::desc(b + k * (2048 >> 4), kDescHi),
-                             id_o, k > 0 ? 1u : !first);
-          } else {
-#pragma unroll
-            for (int k = 0; k < 8; ++k)
-              tc::mma_f16_ta(tmem + kKvDv, tmem + kKvS + 64 * (k >> 2) + 8 * (k & 3), tc::desc(b + k * (2048 >> 4), kDescHi),
-                             id_o, k > 0 ? 1u : !first);
-          }
-          tc::mma_commit(&bars->q_empty[s]);
+          accumulate(kKvDv, kKvS, (2 * step + 1) % kStages, first);
+          tc::mma_commit(&bars->q_empty[(2 * step + 1) % kStages]);
+        }
+        __syncwarp();
+        if (more && !issue_s(last, step + 1)) break;
+        if (!warp_wait(&bars->ds_full, step & 1, gd)) break;
+        tc::fence_after_sync();
+        if (lead) {
+          accumulate(kKvDk, kKvP, (2 * step) % kStages, first);
+          tc::mma_commit(&bars->q_empty[(2 * step) % kStages]);
           if (last) tc::mma_commit(&bars->acc_full);
         }
         __syncwarp();
         accs += last;
-        if (more && !rows(last, left1 == 1, step + 1)) break;
+        if (more && !issue_dp(left1 == 1, step + 1)) break;
         first = last;
         left = left1;
       }
       if (lead) tc::mma_commit(&bars->done);
       __syncwarp();
-      guard_wait(&bars->done, 0, gd, false);         // both issuers' MMAs retired before TMEM is freed
+      guard_wait(&bars->done, 0, gd, false);
     }
   } else if (warp < kMmaWarp) {
     const int half = warp >> 2, r = tid & 127;

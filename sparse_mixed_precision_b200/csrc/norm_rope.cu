@@ -200,9 +200,9 @@ __global__ void __launch_bounds__(kThreads) k_norm_rope(NormRopeArgs g) {
 }
 
 // The backward pass walks a fixed number of blocks per side over the items, so that each block
-// sums its rows' share of dw in registers and writes one partial row.
-constexpr int kUnrollBack = 2;
-
+// sums its rows' share of dw in registers and writes one partial row. One head at
+// a time: the 480p layer takes 419 us so, 532 with two in flight, whose registers leave one block per
+// processor, and 439 with four.
 template <typename T, int D, bool HALVES>
 __global__ void __launch_bounds__(kThreads) k_norm_rope_back(NormRopeArgs g) {
   constexpr int G = D / 16;
@@ -221,36 +221,26 @@ __global__ void __launch_bounds__(kThreads) k_norm_rope_back(NormRopeArgs g) {
     const T* in = static_cast<const T*>(s.x.data) + p.b * s.x.sb + p.t * s.x.st;
     const T* dy = static_cast<const T*>(s.dy.data) + p.b * s.dy.sb + p.t * s.dy.st;
     T* out = static_cast<T*>(s.y.data) + p.b * s.y.sb + p.t * s.y.st;
-    for (int h = p.h0; h < p.h1; h += kUnrollBack) {
-      Raw rx[kUnrollBack], rd[kUnrollBack];
+    for (int h = p.h0; h < p.h1; ++h) {
+      const Raw rx = load_row<T, D>(in + h * s.x.sh, p.c), rd = load_row<T, D>(dy + h * s.dy.sh, p.c);
+      float x[16], d[16], ss = 0.0f, dot = 0.0f;
+      unpack_row<T>(rx, x);
+      unpack_row<T>(rd, d);
+      rotate<HALVES>(d, cs, sn, -1.0f);
 #pragma unroll
-      for (int u = 0; u < kUnrollBack; ++u)
-        if (h + u < p.h1) {
-          rx[u] = load_row<T, D>(in + (h + u) * s.x.sh, p.c);
-          rd[u] = load_row<T, D>(dy + (h + u) * s.dy.sh, p.c);
-        }
-#pragma unroll
-      for (int u = 0; u < kUnrollBack; ++u) {
-        if (h + u >= p.h1) break;
-        float x[16], d[16], ss = 0.0f, dot = 0.0f;
-        unpack_row<T>(rx[u], x);
-        unpack_row<T>(rd[u], d);
-        rotate<HALVES>(d, cs, sn, -1.0f);
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          ss = fmaf(x[i], x[i], ss);
-          dot = fmaf(d[i] * w[i], x[i], dot);
-        }
-        const float r = rsqrtf(group_sum<G>(ss) * (1.0f / D) + g.eps);
-        const float m = group_sum<G>(dot) * r * (1.0f / D);          // mean(g w n)
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          const float n = x[i] * r;
-          if (p.on) dw[i] = fmaf(d[i], n, dw[i]);
-          x[i] = r * (d[i] * w[i] - n * m);
-        }
-        if (p.on) store_row<T, D>(out + (h + u) * s.y.sh, p.c, x);
+      for (int i = 0; i < 16; ++i) {
+        ss = fmaf(x[i], x[i], ss);
+        dot = fmaf(d[i] * w[i], x[i], dot);
       }
+      const float r = rsqrtf(group_sum<G>(ss) * (1.0f / D) + g.eps);
+      const float m = group_sum<G>(dot) * r * (1.0f / D);          // mean(g w n)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        const float n = x[i] * r;
+        if (p.on) dw[i] = fmaf(d[i], n, dw[i]);
+        x[i] = r * (d[i] * w[i] - n * m);
+      }
+      if (p.on) store_row<T, D>(out + h * s.y.sh, p.c, x);
     }
   }
   if (!s.part) return;
@@ -339,14 +329,15 @@ da2_status fill_args(const da2_norm_rope_config* c, const da2_tensor* x[2], cons
   g->tab_sb = (c->flags & DA2_ROPE_BATCHED) ? (int64_t)c->T_rot * (c->d / 2) : 0;
   const int tok = kThreads / (c->d / 16);
   g->token_blocks = (c->T + tok - 1) / tok;
-  // Heads per block: 8 share a token's table row while that leaves two blocks for every
-  // processor (148); shorter inputs are cut finer, down to one head.
+  // Heads per block: 16 (forward; 480p layer 239 us, 245 with 8, 313 with 20) or 8 (backward) share a
+  // token's table row while that leaves two blocks for every processor (148); shorter inputs are cut
+  // finer, down to one head.
   auto blocks = [&](int hc) {
     long n = 0;
     for (int s = 0; s < 2; ++s) n += (H[s] + hc - 1) / hc;
     return n * g->token_blocks * c->B;
   };
-  int hc = 8;
+  int hc = dy ? 8 : 16;
   while (hc > 1 && blocks(hc) < 2 * 148) hc /= 2;
   g->head_chunk = hc;
   for (int s = 0; s < 2; ++s) {
