@@ -42,7 +42,7 @@ struct CrossArgs {
 
 // Boxes of 64 channels and 128 rows.
 struct CrossMaps {
-  CUtensorMap q, k, v, dout, out;
+  CUtensorMap q, k, v, dout, out, dq;
 };
 
 cudaError_t launch_cross_forward(const CrossArgs& g, const CrossMaps& m, bool bf16, cudaStream_t st);

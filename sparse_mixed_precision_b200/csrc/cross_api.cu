@@ -228,6 +228,8 @@ da2_status da2_cross_attention_backward(const da2_cross_config* cfg, const da2_t
   if (e == cudaSuccess) e = make_map(&m.k, in[1], cfg->B, cfg->Hkv, cfg->Tk, cfg->d, bf16);
   if (e == cudaSuccess) e = make_map(&m.v, in[2], cfg->B, cfg->Hkv, cfg->Tk, cfg->d, bf16);
   if (e == cudaSuccess) e = make_map(&m.dout, g.dout, cfg->B, cfg->H, cfg->Tq, cfg->d, bf16);
+  if (e == cudaSuccess) e = make_map(&m.out, g.out, cfg->B, cfg->H, cfg->Tq, cfg->d, bf16);
+  if (e == cudaSuccess) e = make_map(&m.dq, g.dq, cfg->B, cfg->H, cfg->Tq, cfg->d, bf16);
   if (e == cudaSuccess) e = launch_cross_backward(g, m, bf16, stream);
   return cuda_status(e);
 }

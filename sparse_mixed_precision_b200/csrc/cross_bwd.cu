@@ -52,13 +52,15 @@ __device__ __forceinline__ void store32(T* dst, const uint32_t* v, float f) {
 // A work item is one 128-row query tile; Q and dout stay in shared memory, key and value tiles
 // come through a ring. 8 softmax warps share each 128 x 128 step: thread (w, r) owns row r and the
 // keys 64 w .. 64 w + 63. S and dP of the next step are multiplied as soon as this step's have been
-// read into registers. D is computed here (dout is in shared memory, out is read once) and left in
-// the workspace, with lse in the log2 domain, padded to whole tiles, for k_cross_dkv.
+// read into registers. D comes from dout and out, both in shared memory; when one key tile holds every
+// key it is sum p dP instead, exact where a row's out is largest against its rounding, and out is not
+// read. D and lse in the log2 domain are left in the workspace, padded to whole tiles, for k_cross_dkv.
+// dq leaves through out's buffer and a tensor-map store.
 template <int D>
 struct SmemDq {
   static constexpr uint32_t kTile = 128 * D * 2;
-  static constexpr int kStages = D == 128 ? 5 : 8;
-  static constexpr uint32_t kDo = kTile, kStage0 = 2 * kTile;
+  static constexpr int kStages = D == 128 ? 4 : 8;
+  static constexpr uint32_t kDo = kTile, kO = 2 * kTile, kStage0 = 3 * kTile;
   static constexpr uint32_t kExch = kStage0 + kStages * kTile;      // [2 halves][128] fp32
   static constexpr uint32_t kBars = kExch + 1024;
   static constexpr uint32_t kBytes = kBars + 384 + 1024;
@@ -67,7 +69,7 @@ struct SmemDq {
 template <int D>
 struct BarsDq {
   uint64_t kv_full[SmemDq<D>::kStages], kv_empty[SmemDq<D>::kStages];
-  uint64_t q_full, q_empty, s_full, s_free, dp_full, dp_free, ds_full[2], ds_free[2], dq_full, dq_free;
+  uint64_t q_full, q_empty, o_full, o_empty, s_full, s_free, dp_full, dp_free, ds_full[2], ds_free[2], dq_full, dq_free;
   uint64_t done;
   uint32_t tmem, abort;
 };
@@ -138,6 +140,8 @@ k_cross_dq(const __grid_constant__ CrossMaps maps, const __grid_constant__ Cross
     }
     tc::mbar_init(&bars->q_full, 1);
     tc::mbar_init(&bars->q_empty, 2 + 8);                // S and dP, and the warps that read dout
+    tc::mbar_init(&bars->o_full, 1);
+    tc::mbar_init(&bars->o_empty, 1);
     tc::mbar_init(&bars->s_full, 1);
     tc::mbar_init(&bars->s_free, 8);
     tc::mbar_init(&bars->dp_full, 1);
@@ -163,7 +167,7 @@ k_cross_dq(const __grid_constant__ CrossMaps maps, const __grid_constant__ Cross
 
   if (warp == kLoadWarp) {
     if (lane == 0) {
-      uint32_t n = 0, q_loads = 0;
+      uint32_t n = 0, q_loads = 0, o_loads = 0;
       bool dead = false;
       auto load = [&](const CUtensorMap* map, int row, int head, int b) {
         const uint32_t s = n % kStages;
@@ -185,12 +189,22 @@ k_cross_dq(const __grid_constant__ CrossMaps maps, const __grid_constant__ Cross
         for (int t = 0; t < w.nt && !dead; ++t) {
           dead = !load(&maps.k, 128 * t, w.h / g.group, w.b);
           if (!dead) dead = !load(&maps.v, 128 * t, w.h / g.group, w.b);
+          // out, once the dq of the item before has left its buffer: behind the first step's tiles, which
+          // do not wait for that
+          if (t == 0 && w.nt > 1 && !dead) {
+            if (q_loads > 1) dead = !guard_wait(&bars->o_empty, (q_loads - 2) & 1, gd);
+            if (dead) break;
+            tc::mbar_arrive_expect_tx(&bars->o_full, S::kTile);
+            load_tile<D>(sm + S::kO, &maps.out, 128 * w.qt, w.h, w.b, &bars->o_full);
+            ++o_loads;
+          }
         }
       }
 #pragma unroll 1
       for (uint32_t s = 0; s < (uint32_t)kStages && s < n; ++s)
         guard_wait(&bars->kv_full[s], ((n - 1 - s) / kStages) & 1, gd, false);
       if (q_loads) guard_wait(&bars->q_full, (q_loads - 1) & 1, gd, false);
+      if (o_loads) guard_wait(&bars->o_full, (o_loads - 1) & 1, gd, false);
     }
   } else if (warp >= kMmaWarp) {
     // Three issuing warps, one per product: a warp's waits stand behind the MMAs it has issued, so that
@@ -257,7 +271,8 @@ k_cross_dq(const __grid_constant__ CrossMaps maps, const __grid_constant__ Cross
     const int half = warp >> 2, r = tid & 127;
     const uint32_t lane_base = tmem + ((uint32_t)((warp & 3) * 32) << 16);
     const float c = g.scale_log2;
-    uint32_t step = 0, n_items = 0;
+    const bool lead = tid == 0;
+    uint32_t step = 0, n_items = 0, o_items = 0;
     // no wait ends this loop early: all 256 threads must meet at the named barrier
     for (int i = blockIdx.x; i < items; i += gridDim.x) {
       const ItemDq w(g, i);
@@ -269,40 +284,44 @@ k_cross_dq(const __grid_constant__ CrossMaps maps, const __grid_constant__ Cross
           for (int k = 0; k < D / 16; ++k) reinterpret_cast<uint4*>(dq)[k] = make_uint4(0u, 0u, 0u, 0u);
         continue;
       }
-      // D: this thread's half of the row of dout (swizzled in shared memory) and of out
       const size_t bh = (size_t)w.b * g.H + w.h;
       const float lse2 = on ? g.lse_in[bh * g.Tq + row] * kLog2E : INFINITY;
-      uint4 o[D / 16];
-      const T* op = static_cast<const T*>(g.out.data) + w.b * g.out.sb + w.h * g.out.sh + row * g.out.st + half * (D / 2);
-#pragma unroll
-      for (int k = 0; k < D / 16; ++k) o[k] = on ? __ldg(reinterpret_cast<const uint4*>(op) + k) : make_uint4(0u, 0u, 0u, 0u);
-      guard_wait(&bars->q_full, n_items & 1, gd);
-      float part = 0.0f;
-#pragma unroll
-      for (int k = 0; k < D / 16; ++k) {
-        const int ch = half * (D / 16) + k;              // 16-byte chunk of the row
-        const uint4 u = *reinterpret_cast<const uint4*>(sm + S::kDo + (ch >> 3) * 16384 + r * 128 +
-                                                        (((ch & 7) ^ (r & 7)) << 4));
-        const uint32_t a[4] = {u.x, u.y, u.z, u.w}, b[4] = {o[k].x, o[k].y, o[k].z, o[k].w};
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float2 x = unpack16<T>(a[e]), y = unpack16<T>(b[e]);
-          part = fmaf(x.x, y.x, fmaf(x.y, y.y, part));
+      float* exch = reinterpret_cast<float*>(sm + S::kExch);
+      // the two halves' parts of D meet; left for k_cross_dkv
+      auto join = [&](float part) {
+        exch[half * 128 + r] = part;
+        asm volatile("bar.sync 1, 256;" ::: "memory");
+        const float d = exch[r] + exch[128 + r];
+        if (half == 0) {
+          const size_t at = bh * (128 * (size_t)g.q_tiles) + row;
+          g.lse2[at] = lse2;
+          g.delta[at] = d;
         }
+        return d;
+      };
+      float delta = 0.0f;
+      if (w.nt > 1) {                                    // this thread's half of the rows of dout and out
+        guard_wait(&bars->q_full, n_items & 1, gd);
+        guard_wait(&bars->o_full, o_items++ & 1, gd);
+        float part = 0.0f;
+#pragma unroll
+        for (int k = 0; k < D / 16; ++k) {
+          const int ch = half * (D / 16) + k;            // 16-byte chunk of the row, swizzled
+          const uint32_t at = (ch >> 3) * 16384 + r * 128 + (((ch & 7) ^ (r & 7)) << 4);
+          const uint4 u = *reinterpret_cast<const uint4*>(sm + S::kDo + at);
+          const uint4 v = *reinterpret_cast<const uint4*>(sm + S::kO + at);
+          const uint32_t a[4] = {u.x, u.y, u.z, u.w}, b[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float2 x = unpack16<T>(a[e]), y = unpack16<T>(b[e]);
+            part = fmaf(x.x, y.x, fmaf(x.y, y.y, part));
+          }
+        }
+        delta = join(part);
       }
       __syncwarp();
       if (lane == 0) tc::mbar_arrive(&bars->q_empty);
-      float* exch = reinterpret_cast<float*>(sm + S::kExch);
-      exch[half * 128 + r] = part;
-      asm volatile("bar.sync 1, 256;" ::: "memory");
-      const float delta = exch[r] + exch[128 + r];
-      asm volatile("bar.sync 1, 256;" ::: "memory");     // read by all before the next item writes
-      if (half == 0) {
-        const size_t at = bh * (128 * (size_t)g.q_tiles) + row;
-        g.lse2[at] = lse2;
-        g.delta[at] = delta;
-      }
-      const f32x2 c2 = pk2(c, c), b2 = pk2(Scale<T>::kLog2 - lse2, Scale<T>::kLog2 - lse2), d2 = pk2(-delta, -delta);
+      const f32x2 c2 = pk2(c, c), b2 = pk2(Scale<T>::kLog2 - lse2, Scale<T>::kLog2 - lse2);
       for (int t = 0; t < w.nt; ++t, ++step) {
         const int keys = w.keys(t) - 64 * half;          // of this thread's 64
         guard_wait(&bars->s_full, step & 1, gd);
@@ -323,21 +342,27 @@ k_cross_dq(const __grid_constant__ CrossMaps maps, const __grid_constant__ Cross
         tc::fence_after_sync();
         tmem_ld64(lane_base + kDqP + 64 * half, pu);
         warp_arrive(&bars->dp_free, lane);
+        if (keys < 64) {                                 // also NaN from behind the length
+#pragma unroll
+          for (int k = 0; k < 64; ++k)
+            if (k >= keys) s[k] = p[k] = 0.0f;
+        }
+        if (w.nt == 1) {
+          f32x2 sum = pk2(0.0f, 0.0f);
+#pragma unroll
+          for (int k = 0; k < 64; k += 2) sum = fma2(pk2(s[k], s[k + 1]), pk2(p[k], p[k + 1]), sum);
+          float x, y;
+          upk2(sum, x, y);
+          delta = join((x + y) * Scale<T>::kInv);
+        }
+        const f32x2 d2 = pk2(-delta, -delta);
         uint32_t ds[32];
 #pragma unroll
         for (int k = 0; k < 64; k += 2) {
           float x, y;
           upk2(mul2(add2(pk2(p[k], p[k + 1]), d2), pk2(s[k], s[k + 1])), x, y);
-          p[k] = x;
-          p[k + 1] = y;
+          ds[k >> 1] = pack16<T>(x, y);
         }
-        if (keys < 64) {                                 // also NaN from behind the length
-#pragma unroll
-          for (int k = 0; k < 64; ++k)
-            if (k >= keys) p[k] = 0.0f;
-        }
-#pragma unroll
-        for (int k = 0; k < 32; ++k) ds[k] = pack16<T>(p[2 * k], p[2 * k + 1]);
         if (step >= 2) {
           guard_wait(&bars->ds_free[step & 1], ((step >> 1) - 1) & 1, gd);
           tc::fence_after_sync();
@@ -349,18 +374,38 @@ k_cross_dq(const __grid_constant__ CrossMaps maps, const __grid_constant__ Cross
       }
       guard_wait(&bars->dq_full, n_items & 1, gd);
       tc::fence_after_sync();
-      uint32_t acc[D / 2];
 #pragma unroll
-      for (int k = 0; k < D / 2; k += 32) tc::tmem_ld32(lane_base + kDqAcc + half * (D / 2) + k, acc + k);
+      for (int c0 = 0; c0 < D / 2; c0 += 32) {
+        uint32_t v[32];
+        tc::tmem_ld32(lane_base + kDqAcc + half * (D / 2) + c0, v);
+        tc::tmem_wait_ld16(v);
+        tc::tmem_wait_ld16(v + 16);
+        if (c0 + 32 == D / 2) warp_arrive(&bars->dq_free, lane);
+        const float f = g.scale * Scale<T>::kInv;
 #pragma unroll
-      for (int k = 0; k < D / 2; k += 16) tc::tmem_wait_ld16(acc + k);
-      warp_arrive(&bars->dq_free, lane);
-      if (on) {
+        for (int k = 0; k < 4; ++k) {
+          const int ch = half * (D / 16) + c0 / 8 + k;
+          uint32_t u[4];
 #pragma unroll
-        for (int k = 0; k < D / 2; k += 32) store32<T>(dq + k, acc + k, g.scale * Scale<T>::kInv);
+          for (int e = 0; e < 4; ++e)
+            u[e] = pack16<T>(__uint_as_float(v[8 * k + 2 * e]) * f, __uint_as_float(v[8 * k + 2 * e + 1]) * f);
+          *reinterpret_cast<uint4*>(sm + S::kO + (ch >> 3) * 16384 + r * 128 + (((ch & 7) ^ (r & 7)) << 4)) =
+              make_uint4(u[0], u[1], u[2], u[3]);
+        }
+      }
+      tc::fence_proxy_async_smem();
+      asm volatile("bar.sync 1, 256;" ::: "memory");
+      if (lead) {
+#pragma unroll
+        for (int c0 = 0; c0 < D; c0 += 64)
+          tc::tma_store_4d(&maps.dq, sm + S::kO + (c0 >> 6) * 16384, c0, 128 * w.qt, w.h, w.b);
+        tc::bulk_commit();
+        tc::bulk_wait_read<0>();
+        tc::mbar_arrive(&bars->o_empty);
       }
       ++n_items;
     }
+    if (lead) tc::bulk_wait_all();
   }
   tc::fence_before_sync();
   __syncthreads();
