@@ -18,8 +18,16 @@
 // Tensor memory: per tile two S buffers of 64 columns and O (d columns). P overwrites its own S as
 // 16-bit pairs and is the A operand of P V; S of the step after next is issued directly behind P V, so
 // that a softmax warp finds its next S ready and only waits for its own arithmetic: the exponentials
-// (16 per cycle and processor) bound a step at 1024 cycles for the pair of tiles. In the last step
-// only the 16-key groups that hold a valid key are multiplied.
+// (16 per cycle and processor) bound a step at 1024 cycles for the pair of tiles, and S with 64 columns
+// takes 48 cycles per MMA where 128 take 64, 1242 cycles for the pair. In the last step only the 16-key
+// groups that hold a valid key are multiplied.
+//
+// Measured, 40 heads, d = 128, bf16, 32760 queries: 512 keys 370 us = 930 TFLOP/s, 2048 keys 1300 us =
+// 1060 TFLOP/s, 64 keys 143 us (the bytes alone take 102). What bounds it now: instruction fetch and
+// hand-offs, about 2000 cycles a step against 1242. Dropped, each slower on the 512-key case: one S
+// buffer of 128 columns per tile (435 us; 510 with the row in registers), one issuing warp, MMAs issued
+// from inside one lane's branch (75 cycles each to issue instead of 16 to 32), polling waits, a degree-4
+// polynomial for an eighth to a half of the exponentials (no gain: they are not the bound).
 #include <type_traits>
 
 #include "cross.cuh"
@@ -35,8 +43,8 @@ constexpr int kStep = 64;                                         // keys per st
 template <int D>
 struct Smem {
   static constexpr uint32_t kQ = 128 * D * 2;                     // per tile
-  static constexpr uint32_t kHalf = kStep * D * 2;
-  static constexpr uint32_t kKv = 2 * kHalf;
+  static constexpr uint32_t kHalf = kStep * D * 2;                // K or V of one step
+  static constexpr uint32_t kKv = 2 * kHalf;                      // per stage: both
   static constexpr int kStages = D == 128 ? 4 : 8;
   static constexpr uint32_t kOut = 2 * kQ;                        // two 64-channel boxes of the epilogue
   static constexpr uint32_t kStage0 = kOut + 2 * 16384;
