@@ -30,17 +30,18 @@ da2_status check_cross_config(const da2_cross_config* c) {
 long q_pairs(const da2_cross_config* c) { return (c->Tq + 255) / 256; }
 
 // Parts that the keys of one query tile are split into, so that few query rows still fill the
-// processors. In units of one 128-key step's time: a wave of items costs its steps plus about one for
-// filling the pipeline and the epilogue, and joining costs about three, plus the parts' traffic.
+// processors. In units of 128 keys' time: a wave of items costs its keys plus about two for filling the
+// pipeline and the epilogue, and joining costs about four, plus the parts' traffic (40 heads, one query,
+// 512 keys: 16.4 us unsplit, 18.4 in two parts).
 int choose_splits(const da2_cross_config* c) {
   const long units = (long)c->B * c->H * q_pairs(c), steps = ((long)c->Tk + 127) / 128;
   if (units >= kSms || steps < 2) return 1;
   int best = 1;
-  double best_cost = (double)(steps + 1);
+  double best_cost = (double)(steps + 2);
   const double rows = c->Tq < 256 ? c->Tq : 256;
   for (long s = 2; s <= steps && s <= 64; ++s) {
     const long waves = (units * s + kSms - 1) / kSms;
-    const double cost = (double)waves * ((steps + s - 1) / s + 1 + rows / 256.0) + 3.0;
+    const double cost = (double)waves * ((steps + s - 1) / s + 2 + rows / 256.0) + 4.0;
     if (cost < best_cost) best_cost = cost, best = (int)s;
   }
   return best;
