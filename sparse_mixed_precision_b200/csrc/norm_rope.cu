@@ -275,6 +275,7 @@ __global__ void __launch_bounds__(1024) k_norm_dw(NormRopeArgs g) {
   if (!s.part) return;
   const int c = threadIdx.x % D, sl = threadIdx.x / D;
   float v = 0.0f;
+#pragma unroll 16                       // loads in flight; the additions keep their order
   for (int i = sl; i < s.blocks; i += kSlices) v += s.part[(size_t)i * D + c];
   red[sl][c] = v;
   __syncthreads();
