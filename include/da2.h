@@ -278,9 +278,9 @@ const char* da2_status_string(da2_status status);
  * Their tensors are given by a base pointer and element strides of batch, head and token
  * (channels are contiguous), so [B,H,T,d], [B,T,H,d] and slices of a fused projection all go
  * in as they are. Base pointers must be 16-byte aligned and strides multiples of 8 elements
- * (DA2_ERR_ALIGNMENT otherwise); the stride of an axis longer than one must be positive
- * (DA2_ERR_INVALID_ARG otherwise: a zero or negative stride would let rows overlap); the
- * stride of an axis of length one is not read. Outputs must not overlap each other or, but
+ * (DA2_ERR_ALIGNMENT otherwise); the stride of an axis longer than one must be at least d
+ * (DA2_ERR_INVALID_ARG otherwise: rows would overlap); the stride of an axis of length one is
+ * not read. Outputs must not overlap each other or, but
  * where a call says otherwise, an input. d is 64 or 128 and the element type bf16 or fp16.
  * Every sum, norm and softmax statistic is fp32; each output is rounded once.
  * The calls are asynchronous on `stream`, allocate nothing, keep nothing between calls and

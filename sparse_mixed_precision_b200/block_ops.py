@@ -268,8 +268,10 @@ def cross_attention_backward(cfg, dout, q, k, v, out, lse, dq, dk, dv, ws, kv_le
 
 def cross_attention_get_error(ws, stream=None) -> int:
     """Reads and clears the error word of a cross_attention workspace (synchronises the stream)."""
-    import torch
-    s = torch.cuda.current_stream() if stream is None else stream
+    torch = _load()
+    if not isinstance(ws, torch.Tensor) or ws.device.type != "cuda":
+        raise ValueError("da2_cross_attention_get_error: ws must be a CUDA tensor")
+    s = torch.cuda.current_stream(ws.device) if stream is None else stream
     word = ctypes.c_uint32()
     with torch.cuda.device(s.device):
         st = _pkg.lib().da2_cross_attention_get_error(ctypes.c_void_p(ws.data_ptr()), ws.numel() * ws.element_size(),

@@ -25,13 +25,13 @@ struct NvtxRange {
 
 // One strided activation: its axes' lengths come from the call's configuration. On success
 // *out holds the tensor with the strides of axes of length one set to zero (never read).
-inline da2_status check_tensor(const da2_tensor* t, long B, long H, long T, da2_tensor* out) {
+inline da2_status check_tensor(const da2_tensor* t, long B, long H, long T, int d, da2_tensor* out) {
   if (!t || !t->data) return DA2_ERR_INVALID_ARG;
   *out = *t;
   if (B == 1) out->sb = 0;
   if (H == 1) out->sh = 0;
   if (T == 1) out->st = 0;
-  if ((B > 1 && t->sb <= 0) || (H > 1 && t->sh <= 0) || (T > 1 && t->st <= 0)) return DA2_ERR_INVALID_ARG;
+  if ((B > 1 && t->sb < d) || (H > 1 && t->sh < d) || (T > 1 && t->st < d)) return DA2_ERR_INVALID_ARG;
   constexpr int64_t kMaxStride = int64_t(1) << 38;   // elements: byte strides stay below 2^40
   if (out->sb >= kMaxStride || out->sh >= kMaxStride || out->st >= kMaxStride) return DA2_ERR_INVALID_ARG;
   if (!aligned16(t->data) || (out->sb & 7) || (out->sh & 7) || (out->st & 7)) return DA2_ERR_ALIGNMENT;

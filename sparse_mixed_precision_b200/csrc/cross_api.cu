@@ -111,9 +111,9 @@ cudaError_t make_map(CUtensorMap* m, const da2_tensor& t, long B, long H, long T
 da2_status common_args(const da2_cross_config* c, const da2_tensor* q, const da2_tensor* k, const da2_tensor* v,
                        const float* lse, const int32_t* kv_len, void* ws, da2_tensor in[3], CrossArgs* g) {
   *g = CrossArgs{};
-  da2_status s = check_tensor(q, c->B, c->H, c->Tq, &in[0]);
-  if (s == DA2_OK) s = check_tensor(k, c->B, c->Hkv, c->Tk, &in[1]);
-  if (s == DA2_OK) s = check_tensor(v, c->B, c->Hkv, c->Tk, &in[2]);
+  da2_status s = check_tensor(q, c->B, c->H, c->Tq, c->d, &in[0]);
+  if (s == DA2_OK) s = check_tensor(k, c->B, c->Hkv, c->Tk, c->d, &in[1]);
+  if (s == DA2_OK) s = check_tensor(v, c->B, c->Hkv, c->Tk, c->d, &in[2]);
   if (s != DA2_OK) return s;
   if (!ws) return DA2_ERR_INVALID_ARG;
   if ((reinterpret_cast<uintptr_t>(ws) & 255u) != 0 || (reinterpret_cast<uintptr_t>(lse) & 3u) != 0 ||
@@ -167,7 +167,7 @@ da2_status da2_cross_attention(const da2_cross_config* cfg, const da2_tensor* q,
   da2_tensor in[3];
   CrossArgs g;
   s = common_args(cfg, q, k, v, lse, kv_len, ws, in, &g);
-  if (s == DA2_OK) s = check_tensor(out, cfg->B, cfg->H, cfg->Tq, &g.out);
+  if (s == DA2_OK) s = check_tensor(out, cfg->B, cfg->H, cfg->Tq, cfg->d, &g.out);
   if (s != DA2_OK) return s;
   const FwdLayout l = fwd_layout(cfg);
   if (ws_bytes < l.total) return DA2_ERR_WORKSPACE;
@@ -206,11 +206,11 @@ da2_status da2_cross_attention_backward(const da2_cross_config* cfg, const da2_t
   da2_tensor in[3];
   CrossArgs g;
   s = common_args(cfg, q, k, v, lse, kv_len, ws, in, &g);
-  if (s == DA2_OK) s = check_tensor(out, cfg->B, cfg->H, cfg->Tq, &g.out);
-  if (s == DA2_OK) s = check_tensor(dout, cfg->B, cfg->H, cfg->Tq, &g.dout);
-  if (s == DA2_OK) s = check_tensor(dq, cfg->B, cfg->H, cfg->Tq, &g.dq);
-  if (s == DA2_OK) s = check_tensor(dk, cfg->B, cfg->Hkv, cfg->Tk, &g.dk);
-  if (s == DA2_OK) s = check_tensor(dv, cfg->B, cfg->Hkv, cfg->Tk, &g.dv);
+  if (s == DA2_OK) s = check_tensor(out, cfg->B, cfg->H, cfg->Tq, cfg->d, &g.out);
+  if (s == DA2_OK) s = check_tensor(dout, cfg->B, cfg->H, cfg->Tq, cfg->d, &g.dout);
+  if (s == DA2_OK) s = check_tensor(dq, cfg->B, cfg->H, cfg->Tq, cfg->d, &g.dq);
+  if (s == DA2_OK) s = check_tensor(dk, cfg->B, cfg->Hkv, cfg->Tk, cfg->d, &g.dk);
+  if (s == DA2_OK) s = check_tensor(dv, cfg->B, cfg->Hkv, cfg->Tk, cfg->d, &g.dv);
   if (s != DA2_OK) return s;
   if (!lse) return DA2_ERR_INVALID_ARG;
   const BwdLayout l = bwd_layout(cfg);

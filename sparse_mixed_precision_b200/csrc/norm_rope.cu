@@ -350,9 +350,9 @@ da2_status fill_args(const da2_norm_rope_config* c, const da2_tensor* x[2], cons
     sd.chunks = (H[s] + hc - 1) / hc;
     sd.items = (long)c->B * g->token_blocks * sd.chunks;
     if (H[s] == 0) continue;
-    da2_status e = check_tensor(x[s], c->B, H[s], c->T, &sd.x);
-    if (e == DA2_OK) e = check_tensor(y[s], c->B, H[s], c->T, &sd.y);
-    if (e == DA2_OK && dy) e = check_tensor(dy[s], c->B, H[s], c->T, &sd.dy);
+    da2_status e = check_tensor(x[s], c->B, H[s], c->T, c->d, &sd.x);
+    if (e == DA2_OK) e = check_tensor(y[s], c->B, H[s], c->T, c->d, &sd.y);
+    if (e == DA2_OK && dy) e = check_tensor(dy[s], c->B, H[s], c->T, c->d, &sd.dy);
     if (e != DA2_OK) return e;
     if (w[s] && !aligned16(w[s])) return DA2_ERR_ALIGNMENT;
     sd.w = w[s];

@@ -50,6 +50,7 @@ def test_bad_arguments_are_refused():
     assert _status(c, q=(0x1008, None)) == 3
     assert _status(c, k=(0x1000, (0, 77 * 64, 64))) == 1           # keys broadcast over the batch
     assert _status(c, out=(0x1000, (4 * 300 * 64, 300 * 64, 68))) == 3
+    assert _status(c, out=(0x1000, (4 * 300 * 64, 300 * 64, 56))) == 1   # rows would overlap
     assert _status(c, ws=None) == 1
     assert _status(c, ws=0x1010) == 3
     assert _status(c, ws_bytes=0) == 4
@@ -73,6 +74,8 @@ def test_binding_checks_tensors():
         da2.cross_attention(cfg, k, k, k, q, ws)
     with pytest.raises(ValueError, match="dtype"):
         da2.cross_attention(cfg, q.float(), k, k, q, ws)
+    with pytest.raises(ValueError, match="CUDA tensor"):
+        da2.cross_attention_get_error(ws)
     with pytest.raises(ValueError, match="dtype"):
         da2.cross_config(1, 1, 1, 1, 64, dtype=torch.float32)
 

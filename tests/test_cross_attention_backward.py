@@ -30,7 +30,7 @@ def test_bad_arguments_are_refused():
     assert _status(c, lse=0x1002) == 3
     assert _status(c, dk=(None, None)) == 1
     assert _status(c, dk=(0x1000, (77 * 64 * 4, 0, 64))) == 1
-    assert _status(c, dk=(0x1000, (77 * 64 * 4, 77 * 64, 60))) == 3
+    assert _status(c, dk=(0x1000, (77 * 64 * 4, 77 * 64, 68))) == 3
     assert _status(c, ws=None) == 1
     assert _status(c, ws=0x1080) == 3
     assert _status(c, ws_bytes=need - 1) == 4

@@ -51,6 +51,7 @@ def test_bad_arguments_are_refused():
     assert _status(_cfg(), cos=0x1004) == 3
     assert _status(_cfg(), strides=(0, 640, 64)) == 1          # broadcast batch
     assert _status(_cfg(), strides=(1920, -640, 64)) == 1
+    assert _status(_cfg(), strides=(1920, 640, 32)) == 1       # rows would overlap
     assert _status(_cfg(), strides=(1920, 640, 68)) == 3       # token stride not a multiple of 8
     c = _cfg()
     c.flags = 4
