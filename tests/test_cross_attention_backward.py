@@ -197,3 +197,28 @@ def test_wait_that_runs_out_is_reported():
     da2.cross_attention_backward(cfg, dout, q, k, v, out, lse, *bad, ws)
     assert da2.cross_attention_get_error(ws) == 0
     assert all(torch.equal(a, b) for a, b in zip(grads, bad))
+
+
+@pytest.mark.gpu
+def test_offsets_past_32_bits():
+    """Tensors of more than 2^31 elements: the last rows of the last head, both directions."""
+    B, H, Tq, Tk, d = 4, 40, 118800, 40, 128
+    gen = torch.Generator(device="cuda").manual_seed(6)
+    q = torch.empty(B, H, Tq, d, dtype=torch.bfloat16, device="cuda").normal_(generator=gen)
+    k, v = (torch.empty(B, H, Tk, d, dtype=torch.bfloat16, device="cuda").normal_(generator=gen) for _ in range(2))
+    cfg = da2.cross_config(B, H, Tq, Tk, d)
+    out, lse = torch.empty_like(q), torch.empty(B, H, Tq, device="cuda")
+    da2.cross_attention(cfg, q, k, v, out, da2.cross_attention_workspace(cfg, "cuda"), lse=lse)
+    last = (slice(B - 1, B), slice(H - 1, H))
+    cut = (*last, slice(Tq - 300, Tq))
+    want = formulas64(q[cut], k[last], v[last], None, "bhtd")
+    check_out(out[cut], lse[cut[:2]][:, :, -300:], want, torch.bfloat16, "bhtd")
+    # the gradient of out is zero but in the rows that are compared: dk and dv come from them alone
+    dout = torch.zeros_like(q)
+    dout[cut] = torch.randn(1, 1, 300, d, generator=gen, device="cuda").to(torch.bfloat16)
+    dq, dk, dv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
+    ws = da2.cross_attention_workspace(cfg, "cuda", backward=True)
+    da2.cross_attention_backward(cfg, dout, q, k, v, out, lse, dq, dk, dv, ws)
+    grads = gradients64(q[cut], k[last], v[last], dout[cut], None, "bhtd", torch.bfloat16)
+    check_grads((dq[cut], dk[last], dv[last]), grads, "bhtd")
+    assert (dq[0, 0] == 0).all() and (dk[0] == 0).all() and (dv[0] == 0).all()
