@@ -40,7 +40,7 @@ struct CrossArgs {
   float* part_kv;                  // fp32 [2 sms][2][d][128]: dK and dV of split sums
 };
 
-// Boxes of 64 channels and 128 rows.
+// Boxes of 64 channels and 128 rows (k and v of the forward pass: 64 rows).
 struct CrossMaps {
   CUtensorMap q, k, v, dout, out, dq;
 };

@@ -133,17 +133,6 @@ __device__ __forceinline__ void fence_after_sync() {
   asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
 }
 
-// Registers per thread of this warpgroup from here on (executed by its four warps). The shares of a
-// block's warpgroups add up to what it was launched with.
-template <int N>
-__device__ __forceinline__ void regs_more() {
-  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
-}
-template <int N>
-__device__ __forceinline__ void regs_less() {
-  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
-}
-
 // ---------------------------------------------------------------- descriptors
 // Shared-memory matrix descriptor, K-major, no swizzle: core matrices of 8 rows x 16 bytes;
 // lbo = byte distance between core matrices adjacent along K, sbo = along M/N.
@@ -163,17 +152,11 @@ __host__ __device__ constexpr uint32_t idesc_nvf4(int M, int N) {
 
 // Descriptors of tiles that a tensor-map load left with the 128-byte swizzle: rows of 64 16-bit
 // elements (128 bytes, 16-byte chunk j of row r at chunk j ^ (r % 8)), 1024-byte aligned, further
-// 64-column boxes behind each other. sdesc_k: the contraction runs along the row (advance 16
-// elements by 32 bytes); sdesc_mn: it runs along the rows (advance 16 rows by 2048 bytes), and
-// box_bytes is the distance between 64-column boxes.
+// 64-column boxes behind each other. High word: kSw128's with 1024 / 16, the distance of 8 rows. Low
+// word: the address / 16 and, above it (bit 16), 1 where the contraction runs along the row (16
+// elements further: 32 bytes), or the distance of 64-column boxes / 16 where it runs along the rows (16
+// rows further: 2048 bytes).
 constexpr uint64_t kSw128 = (1ull << 46) | (2ull << 61);
-__device__ __forceinline__ uint64_t sdesc_k(const void* smem) {
-  return (uint64_t)((smem_u32(smem) & 0x3FFFFu) >> 4) | (1ull << 16) | ((uint64_t)(1024 >> 4) << 32) | kSw128;
-}
-__device__ __forceinline__ uint64_t sdesc_mn(const void* smem, uint32_t box_bytes) {
-  return (uint64_t)((smem_u32(smem) & 0x3FFFFu) >> 4) | ((uint64_t)((box_bytes >> 4) & 0x3FFFu) << 16) |
-         ((uint64_t)(1024 >> 4) << 32) | kSw128;
-}
 // Instruction descriptor, kind::f16 with bf16 or fp16 A and B, fp32 accumulate, A K-major, B
 // K-major or (b_mn) MN-major.
 __host__ __device__ constexpr uint32_t idesc_f16(bool bf16, int M, int N, bool b_mn) {
