@@ -303,9 +303,11 @@ k_cross_dq(const __grid_constant__ CrossMaps maps, const __grid_constant__ Cross
         }
         return d;
       };
+      // Also where the rows are not read here: q_full of this item completes only behind the item
+      // before's phase of q_empty, so that no arrival below can count into that phase.
+      guard_wait(&bars->q_full, n_items & 1, gd);
       float delta = 0.0f;
       if (w.nt > 1) {                                    // this thread's half of the rows of dout and out
-        guard_wait(&bars->q_full, n_items & 1, gd);
         guard_wait(&bars->o_full, o_items++ & 1, gd);
         float part = 0.0f;
 #pragma unroll
