@@ -33,11 +33,12 @@ struct CrossArgs {
   int q_pairs, splits;             // 256-row query tiles per head; parts of the keys
   float *part_o, *part_lse;        // fp32 [splits][B*H*Tq][d], [splits][B*H*Tq] (log2 domain)
   // backward
-  da2_tensor dout, dq, dk, dv;
+  da2_tensor v, dout, dq, dk, dv;
   const float* lse_in;
   int q_tiles, k_tiles;            // 128-row tiles
   float *lse2, *delta;             // fp32 [B*H][128 q_tiles]: lse in the log2 domain, D
   float* part_kv;                  // fp32 [2 sms][2][d][128]: dK and dV of split sums
+  float *dnorm2, *vnorm2;          // fp16: [B*H][q_tiles][4] and [B*Hkv][k_tiles], largest squared row norms
 };
 
 // Boxes of 64 channels and 128 rows (k and v of the forward pass: 64 rows).

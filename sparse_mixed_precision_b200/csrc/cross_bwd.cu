@@ -13,8 +13,13 @@
 // change of query tiles (about 5000 cycles against 2000 a step of 1540 of MMA time).
 //
 // p and dS are rounded once to the 16-bit type as MMA operands (fp32 accumulators). In fp16 both
-// carry a factor of 2^6, taken out of the accumulators: with many keys p and dS fall below fp16's
-// smallest normal 2^-14 otherwise, while |dS| stays in range up to 1023.
+// carry a power of two, taken out of the accumulators: with many keys they fall below fp16's smallest
+// normal 2^-14 otherwise. p <= 1 carries 2^6. |dS| <= |dP| + |D| <= 2 |dout row| |v row| by Cauchy and
+// Schwarz, and D of a rounded out stays within 1 % of that; so dS carries 2^(13 - E), 2^E <= the bound
+// |dout row| max |v row| < 2^(E+1), and stays below 33100 whatever dout's size (a fixed 2^6 overflowed at
+// |dS| = 1024). In dq each query row has its own power; in dk, whose sums run over the queries, all query
+// rows of a key/value head share the smallest. k_cross_vnorm leaves the value rows' largest norm of
+// each key tile, k_cross_dq the dout rows' of each query tile.
 #include <type_traits>
 
 #include "cross.cuh"
@@ -29,9 +34,81 @@ constexpr int kMmaWarp = 8, kLoadWarp = 11;             // warps 8 to 10 issue M
 template <typename T>
 struct Scale {
   static constexpr bool kBf16 = std::is_same<T, __nv_bfloat16>::value;
-  static constexpr float kLog2 = kBf16 ? 0.0f : 6.0f;      // of p and dS
+  static constexpr float kLog2 = kBf16 ? 0.0f : 6.0f;      // of p
   static constexpr float kInv = kBf16 ? 1.0f : 1.0f / 64.0f;
 };
+
+__device__ __forceinline__ float pow2(int e) { return __int_as_float((127 + e) << 23); }
+// Largest of a warp's squared norms: non-negative floats compare like their bits, NaN above all.
+__device__ __forceinline__ float warp_max(float x) {
+  return __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(x)));
+}
+// The exponent of dS in fp16: 13 - E, from the squared norms of the dout row and the largest value row.
+// E is kept above -40 (gradients that small are zero in fp16); an infinite or NaN norm, whose row's
+// gradients are not finite, gives E = 64.
+__device__ __forceinline__ int ds_exponent(float dout2, float v2) {
+  const int e = (int)(__float_as_uint(dout2 * v2) >> 23 & 0xFF) - 127;
+  return 13 - max(e >> 1, -40);
+}
+// A lane's share of the largest squared norm of a value row among the valid key tiles of one key/value
+// head (warp_max joins the lanes), and the same of dout over every query tile of the query heads that
+// share the head, four parts per tile.
+__device__ __forceinline__ float value_norm2(const CrossArgs& g, int b, int hkv, int tiles, int lane) {
+  const float* at = g.vnorm2 + ((size_t)b * g.Hkv + hkv) * g.k_tiles;
+  float m = 0.0f;
+#pragma unroll 1
+  for (int t = lane; t < tiles; t += 32) m = fmaxf(m, at[t]);
+  return m;
+}
+__device__ __forceinline__ float dout_norm2(const CrossArgs& g, int b, int hkv, int lane) {
+  const float4* at = reinterpret_cast<const float4*>(g.dnorm2) + ((size_t)b * g.H + (size_t)hkv * g.group) * g.q_tiles;
+  const int n = g.group * g.q_tiles;
+  float m = 0.0f;
+#pragma unroll 4
+  for (int t = lane; t < n; t += 32) {
+    const float4 x = at[t];
+    m = fmaxf(m, fmaxf(fmaxf(x.x, x.y), fmaxf(x.z, x.w)));
+  }
+  return m;
+}
+
+// Squared norms of the value rows, the largest of each key tile's valid rows (fp16 only). D / 8 lanes
+// share a row.
+template <int D>
+__global__ void __launch_bounds__(256) k_cross_vnorm(const __grid_constant__ CrossArgs g) {
+  __shared__ float red[8];
+  constexpr int G = D / 8;
+  asm volatile("griddepcontrol.launch_dependents;");     // k_cross_dq may start; it waits before it reads
+  const int kt = blockIdx.x % g.k_tiles, bh = blockIdx.x / g.k_tiles, b = bh / g.Hkv, hkv = bh - b * g.Hkv;
+  const int end = min(valid_keys(g, b), 128 * (kt + 1)), c = threadIdx.x % G;
+  const __half* v = static_cast<const __half*>(g.v.data) + b * g.v.sb + hkv * g.v.sh + 8 * c;
+  float m = 0.0f;
+#pragma unroll
+  for (int r = 0; r < 128; r += 256 / G) {
+    const int key = 128 * kt + r + threadIdx.x / G;
+    float n2 = 0.0f;
+    if (key < g.Tk) {                                    // before the length is known: one latency, not two
+      const uint4 u = __ldg(reinterpret_cast<const uint4*>(v + key * g.v.st));
+      const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float2 x = unpack16<__half>(w[e]);
+        n2 = fmaf(x.x, x.x, fmaf(x.y, x.y, n2));
+      }
+    }
+#pragma unroll
+    for (int o = 1; o < G; o <<= 1) n2 += __shfl_xor_sync(0xffffffffu, n2, o);
+    if (key < end) m = fmaxf(m, n2);
+  }
+  m = warp_max(m);
+  if (threadIdx.x % 32 == 0) red[threadIdx.x / 32] = m;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+#pragma unroll
+    for (int i = 1; i < 8; ++i) m = fmaxf(m, red[i]);
+    g.vnorm2[blockIdx.x] = m;
+  }
+}
 
 __device__ __forceinline__ void tmem_ld64(uint32_t taddr, uint32_t* v) {
   tc::tmem_ld32(taddr, v);
@@ -65,9 +142,9 @@ struct SmemDq {
   static constexpr uint32_t kTile = 128 * D * 2;
   static constexpr int kStages = D == 128 ? 4 : 8;
   static constexpr uint32_t kDo = kTile, kO = 2 * kTile, kStage0 = 3 * kTile;
-  static constexpr uint32_t kExch = kStage0 + kStages * kTile;      // [2 halves][128] fp32
-  static constexpr uint32_t kBars = kExch + 1024;
-  static constexpr uint32_t kBytes = kBars + 384 + 1024;
+  static constexpr uint32_t kExch = kStage0 + kStages * kTile;      // [D, norm][2 halves][128] fp32
+  static constexpr uint32_t kBars = kExch + 2048;
+  static constexpr uint32_t kBytes = kBars + 384;
   static_assert(kBytes <= 232448, "shared memory budget");
 };
 template <int D>
@@ -130,12 +207,15 @@ k_cross_dq(const __grid_constant__ CrossMaps maps, const __grid_constant__ Cross
   using S = SmemDq<D>;
   constexpr int kStages = S::kStages;
   constexpr bool kBf16 = Scale<T>::kBf16;
-  extern __shared__ uint8_t sm_raw[];
-  uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(sm_raw) + 1023) & ~uintptr_t(1023));
+  extern __shared__ __align__(1024) uint8_t sm[];
   BarsDq<D>* bars = reinterpret_cast<BarsDq<D>*>(sm + S::kBars);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int items = g.B * g.H * g.q_tiles;
   const Guard gd{g.err, &bars->abort, g.wait_clocks};
+  if (tc::smem_u32(sm) & 1023u) {        // the swizzle needs the alignment that the declaration asks for
+    if (tid == 0) set_error(g.err, kErrBadIndex);
+    return;
+  }
 
   if (tid == 0) {
     for (int s = 0; s < kStages; ++s) {
@@ -277,6 +357,17 @@ k_cross_dq(const __grid_constant__ CrossMaps maps, const __grid_constant__ Cross
     const float c = g.scale_log2;
     const bool lead = tid == 0;
     uint32_t step = 0, n_items = 0, o_items = 0;
+    float v2 = 0.0f;                       // the next item's value norm, read ahead
+    auto ahead = [&](int i) {
+      if constexpr (!kBf16) {
+        if (i < items) {
+          const ItemDq w(g, i);
+          v2 = value_norm2(g, w.b, w.h / g.group, w.nt, lane);
+        }
+      }
+    };
+    if constexpr (!kBf16) asm volatile("griddepcontrol.wait;" ::: "memory");     // for k_cross_vnorm
+    ahead(blockIdx.x);
     // no wait ends this loop early: all 256 threads must meet at the named barrier
     for (int i = blockIdx.x; i < items; i += gridDim.x) {
       const ItemDq w(g, i);
@@ -286,14 +377,18 @@ k_cross_dq(const __grid_constant__ CrossMaps maps, const __grid_constant__ Cross
       if (w.nt == 0) {
         if (on)
           for (int k = 0; k < D / 16; ++k) reinterpret_cast<uint4*>(dq)[k] = make_uint4(0u, 0u, 0u, 0u);
+        ahead(i + gridDim.x);
         continue;
       }
       const size_t bh = (size_t)w.b * g.H + w.h;
       const float lse2 = on ? g.lse_in[bh * g.Tq + row] * kLog2E : INFINITY;
       float* exch = reinterpret_cast<float*>(sm + S::kExch);
-      // the two halves' parts of D meet; left for k_cross_dkv
+      // the two halves' parts of D, and of the norm of dout's row in fp16, meet; left for k_cross_dkv
+      int ex = 0;                                        // of dS
+      float n2 = 0.0f;
       auto join = [&](float part) {
         exch[half * 128 + r] = part;
+        if constexpr (!kBf16) exch[256 + half * 128 + r] = n2;
         asm volatile("bar.sync 1, 256;" ::: "memory");
         const float d = exch[r] + exch[128 + r];
         if (half == 0) {
@@ -301,18 +396,39 @@ k_cross_dq(const __grid_constant__ CrossMaps maps, const __grid_constant__ Cross
           g.lse2[at] = lse2;
           g.delta[at] = d;
         }
+        if constexpr (!kBf16) {
+          n2 = exch[256 + r] + exch[384 + r];
+          ex = ds_exponent(n2, v2);
+          const float tile2 = warp_max(n2);
+          if (half == 0 && lane == 0) g.dnorm2[(bh * g.q_tiles + w.qt) * 4 + warp] = tile2;
+        }
         return d;
       };
       // Also where the rows are not read here: q_full of this item completes only behind the item
       // before's phase of q_empty, so that no arrival below can count into that phase.
       guard_wait(&bars->q_full, n_items & 1, gd);
       float delta = 0.0f;
+      if constexpr (!kBf16) {
+        v2 = warp_max(v2);
+#pragma unroll
+        for (int k = 0; k < D / 16; ++k) {
+          const int ch = half * (D / 16) + k;            // 16-byte chunk of the row, swizzled
+          const uint4 u = *reinterpret_cast<const uint4*>(sm + S::kDo + (ch >> 3) * 16384 + r * 128 +
+                                                          (((ch & 7) ^ (r & 7)) << 4));
+          const uint32_t a[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float2 x = unpack16<T>(a[e]);
+            n2 = fmaf(x.x, x.x, fmaf(x.y, x.y, n2));
+          }
+        }
+      }
       if (w.nt > 1) {                                    // this thread's half of the rows of dout and out
         guard_wait(&bars->o_full, o_items++ & 1, gd);
         float part = 0.0f;
 #pragma unroll
         for (int k = 0; k < D / 16; ++k) {
-          const int ch = half * (D / 16) + k;            // 16-byte chunk of the row, swizzled
+          const int ch = half * (D / 16) + k;
           const uint32_t at = (ch >> 3) * 16384 + r * 128 + (((ch & 7) ^ (r & 7)) << 4);
           const uint4 u = *reinterpret_cast<const uint4*>(sm + S::kDo + at);
           const uint4 v = *reinterpret_cast<const uint4*>(sm + S::kO + at);
@@ -327,7 +443,7 @@ k_cross_dq(const __grid_constant__ CrossMaps maps, const __grid_constant__ Cross
       }
       __syncwarp();
       if (lane == 0) tc::mbar_arrive(&bars->q_empty);
-      const f32x2 c2 = pk2(c, c), b2 = pk2(Scale<T>::kLog2 - lse2, Scale<T>::kLog2 - lse2);
+      const f32x2 c2 = pk2(c, c), b2 = pk2(-lse2, -lse2);
       for (int t = 0; t < w.nt; ++t, ++step) {
         const int keys = w.keys(t) - 64 * half;          // of this thread's 64
         guard_wait(&bars->s_full, step & 1, gd);
@@ -359,14 +475,15 @@ k_cross_dq(const __grid_constant__ CrossMaps maps, const __grid_constant__ Cross
           for (int k = 0; k < 64; k += 2) sum = fma2(pk2(s[k], s[k + 1]), pk2(p[k], p[k + 1]), sum);
           float x, y;
           upk2(sum, x, y);
-          delta = join((x + y) * Scale<T>::kInv);
+          delta = join(x + y);
         }
-        const f32x2 d2 = pk2(-delta, -delta);
+        const f32x2 f2 = pk2(pow2(ex), pow2(ex)), d2 = pk2(-delta * pow2(ex), -delta * pow2(ex));
         uint32_t ds[32];
 #pragma unroll
         for (int k = 0; k < 64; k += 2) {
+          const f32x2 dp = pk2(p[k], p[k + 1]);
           float x, y;
-          upk2(mul2(add2(pk2(p[k], p[k + 1]), d2), pk2(s[k], s[k + 1])), x, y);
+          upk2(mul2(kBf16 ? add2(dp, d2) : fma2(dp, f2, d2), pk2(s[k], s[k + 1])), x, y);
           ds[k >> 1] = pack16<T>(x, y);
         }
         if (step >= 2) {
@@ -378,6 +495,7 @@ k_cross_dq(const __grid_constant__ CrossMaps maps, const __grid_constant__ Cross
         tc::tmem_wait_st();
         warp_arrive(&bars->ds_full[step & 1], lane);
       }
+      ahead(i + gridDim.x);
       guard_wait(&bars->dq_full, n_items & 1, gd);
       tc::fence_after_sync();
 #pragma unroll
@@ -387,7 +505,7 @@ k_cross_dq(const __grid_constant__ CrossMaps maps, const __grid_constant__ Cross
         tc::tmem_wait_ld16(v);
         tc::tmem_wait_ld16(v + 16);
         if (c0 + 32 == D / 2) warp_arrive(&bars->dq_free, lane);
-        const float f = g.scale * Scale<T>::kInv;
+        const float f = g.scale * pow2(-ex);
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
           const int ch = half * (D / 16) + c0 / 8 + k;
@@ -647,6 +765,14 @@ k_cross_dkv(const __grid_constant__ CrossMaps maps, const __grid_constant__ Cros
       const long end = min(u1, (gi + 1) * sh.n);
       const bool whole = u == gi * sh.n && end == (gi + 1) * sh.n;
       const int slot = 2 * blockIdx.x + (u == u0 ? 0 : 1);
+      int ex = 0;                                        // of dS
+      if constexpr (!kBf16) {
+        const Group w(g, gi);
+        const float v2 = value_norm2(g, w.b, w.hkv, (w.len + 127) >> 7, lane);
+        ex = ds_exponent(warp_max(dout_norm2(g, w.b, w.hkv, lane)), warp_max(v2));
+      }
+      // p carries 2^kLog2 already
+      const f32x2 f2 = pk2(pow2(ex) * Scale<T>::kInv, pow2(ex) * Scale<T>::kInv);
       for (; u < end; ++u, ++step) {
         const uint32_t n = 2 * step, st = n % kStages;
         const float4* vec = reinterpret_cast<const float4*>(sm + S::kVec + st / 2 * 1024 + half * 256);
@@ -682,9 +808,11 @@ k_cross_dkv(const __grid_constant__ CrossMaps maps, const __grid_constant__ Cros
 #pragma unroll
         for (int k = 0; k < 64; k += 4) {
           const float4 d = vec[32 + k / 4];
+          f32x2 a = add2(pk2(p[k], p[k + 1]), pk2(-d.x, -d.y)), b = add2(pk2(p[k + 2], p[k + 3]), pk2(-d.z, -d.w));
+          if constexpr (!kBf16) a = mul2(a, f2), b = mul2(b, f2);
           float x0, x1, x2, x3;
-          upk2(mul2(add2(pk2(p[k], p[k + 1]), pk2(-d.x, -d.y)), pk2(s[k], s[k + 1])), x0, x1);
-          upk2(mul2(add2(pk2(p[k + 2], p[k + 3]), pk2(-d.z, -d.w)), pk2(s[k + 2], s[k + 3])), x2, x3);
+          upk2(mul2(a, pk2(s[k], s[k + 1])), x0, x1);
+          upk2(mul2(b, pk2(s[k + 2], s[k + 3])), x2, x3);
           w16[k / 2] = pack16<T>(x0, x1);
           w16[k / 2 + 1] = pack16<T>(x2, x3);
         }
@@ -698,7 +826,7 @@ k_cross_dkv(const __grid_constant__ CrossMaps maps, const __grid_constant__ Cros
       tc::fence_after_sync();
       const Group w(g, gi);
       const int key = 128 * w.kt + r;
-      const float f = (half ? g.scale : 1.0f) * Scale<T>::kInv;
+      const float f = half ? g.scale * pow2(-ex) : Scale<T>::kInv;
       const da2_tensor& out = half ? g.dk : g.dv;
       T* row = static_cast<T*>(out.data) + w.b * out.sb + w.hkv * out.sh + key * out.st;
       float* part = g.part_kv + ((size_t)slot * 2 + half) * D * 128 + r;
@@ -773,9 +901,23 @@ cudaError_t launch(const CrossArgs& g, const CrossMaps& m, cudaStream_t st) {
     e = cudaFuncSetAttribute(k_cross_dkv<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              (int)SmemDkv<D>::kBytes);
   if (e != cudaSuccess) return e;
+  if constexpr (!Scale<T>::kBf16) {
+    k_cross_vnorm<D><<<(unsigned)(g.B * g.Hkv * g.k_tiles), 256, 0, st>>>(g);
+    e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+  }
   const int items = g.B * g.H * g.q_tiles;
-  k_cross_dq<T, D><<<items < g.sms ? items : g.sms, kThreads, SmemDq<D>::kBytes, st>>>(m, g);
-  e = cudaGetLastError();
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(items < g.sms ? items : g.sms);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = SmemDq<D>::kBytes;
+  cfg.stream = st;
+  cudaLaunchAttribute early = {};                        // of k_cross_dq over k_cross_vnorm
+  early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  early.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &early;
+  cfg.numAttrs = Scale<T>::kBf16 ? 0 : 1;
+  e = cudaLaunchKernelEx(&cfg, k_cross_dq<T, D>, m, g);
   if (e != cudaSuccess) return e;
   k_cross_dkv<T, D><<<g.sms, kThreads, SmemDkv<D>::kBytes, st>>>(m, g);
   e = cudaGetLastError();

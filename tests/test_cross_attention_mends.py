@@ -25,3 +25,108 @@ def test_many_query_tiles_of_one_key_tile(Tk, lens):
         da2.cross_attention_backward(cfg, dout, q, k, v, out, lse, *again, ws, kv_len=kv_len)
         assert all(torch.equal(a, b) for a, b in zip(grads, again))
     assert da2.cross_attention_get_error(ws) == 0
+
+
+# ------------------------------------------------------------------ gradients over fp16's range
+def fp16_wants(q, k, v, dout, lens):
+    """gradients64 plus what dS may lose below fp16's smallest normal. dS is rounded with a power of two
+    of at least 2^13 / bound, bound = max |dout row| max |v row| over the query heads of a key/value
+    head, so that a subnormal is off by at most 2^-25 2^-13 bound."""
+    want = gradients64(q, k, v, dout, lens, "bhtd", torch.float16)
+    B, H, Tq, d = q.shape
+    Hkv = k.shape[1]
+    for b in range(B):
+        n = k.shape[2] if lens is None else lens[b]
+        if n == 0:
+            continue
+        rows = dout[b].double().norm(dim=-1).view(Hkv, -1).amax(-1)
+        tiny = (rows * v[b, :, :n].double().norm(dim=-1).amax(-1) * 2.0 ** -38 / d ** 0.5)[:, None, None]
+        want[0][1][b] += (tiny * k[b, :, :n].double().abs().sum(1, keepdim=True)).repeat_interleave(H // Hkv, 0)
+        want[1][1][b, :, :n] += tiny * q[b].double().abs().view(Hkv, -1, d).sum(1, keepdim=True)
+    return want
+
+
+FP16_CASES = [  # B, H, Hkv, Tq, Tk, d, lens
+    (1, 2, 2, 200, 16, 128, None), (2, 4, 2, 130, 77, 128, [77, 5]), (1, 2, 1, 300, 512, 128, None),
+    (2, 2, 2, 150, 300, 64, [300, 129]),
+]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("case", FP16_CASES)
+@pytest.mark.parametrize("scale", [2.0 ** 9, 300.0, 2.0 ** -9, 2.0 ** -14])
+def test_fp16_gradients_of_large_and_small_dout(case, scale):
+    """|dS| far above 1023 and far below fp16's normals, as loss scaling leaves them: the gradients are
+    ordinary fp16 numbers throughout."""
+    B, H, Hkv, Tq, Tk, d, lens = case
+    q, k, v, kv_len = make(B, H, Hkv, Tq, Tk, d, torch.float16, "bhtd", lens)
+    g = torch.Generator(device="cuda").manual_seed(9)
+    dout = (torch.randn(q.shape, generator=g, device="cuda") * scale).half()
+    cfg = da2.cross_config(B, H, Tq, Tk, d, Hkv=Hkv, dtype=torch.float16)
+    _, _, grads = run_both(cfg, q, k, v, dout, kv_len)
+    want = fp16_wants(q, k, v, dout, lens)
+    assert all(x.abs().max() < 65504 for x, _ in want)
+    check_grads(grads, want, "bhtd")
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("case", FP16_CASES)
+def test_fp16_gradients_of_uneven_rows(case):
+    """One row of dout 2^8 and one value row 2^3 times the others."""
+    B, H, Hkv, Tq, Tk, d, lens = case
+    q, k, v, kv_len = make(B, H, Hkv, Tq, Tk, d, torch.float16, "bhtd", lens, seed=5)
+    dout = torch.randn(q.shape, generator=torch.Generator(device="cuda").manual_seed(2), device="cuda").half()
+    dout[:, 0, 70] *= 2.0 ** 8
+    v[:, :, 3] *= 2.0 ** 3
+    cfg = da2.cross_config(B, H, Tq, Tk, d, Hkv=Hkv, dtype=torch.float16)
+    _, _, grads = run_both(cfg, q, k, v, dout, kv_len)
+    check_grads(grads, fp16_wants(q, k, v, dout, lens), "bhtd")
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("Tk", [90, 300])
+@pytest.mark.parametrize("bad", [float("inf"), float("nan")])
+def test_fp16_infinite_gradient_stays_where_it_belongs(Tk, bad):
+    """An overflowed element of dout, as loss scaling meets them: its row of dq and its head's dk and
+    dv say so, every other row of dq and the other head are as without it."""
+    q, k, v, _ = make(1, 2, 2, 260, Tk, 128, torch.float16, "bhtd", None, seed=6)
+    dout = torch.randn(q.shape, generator=torch.Generator(device="cuda").manual_seed(3), device="cuda").half()
+    cfg = da2.cross_config(1, 2, 260, Tk, 128, dtype=torch.float16)
+    out, lse, clean = run_both(cfg, q, k, v, dout, None)
+    dout[0, 0, 150, 7] = bad
+    dq, dk, dv = (torch.empty_like(x) for x in clean)
+    ws = da2.cross_attention_workspace(cfg, "cuda", backward=True)
+    da2.cross_attention_backward(cfg, dout, q, k, v, out, lse, dq, dk, dv, ws)
+    assert not torch.isfinite(dq[0, 0, 150]).any() and not torch.isfinite(dk[0, 0]).any()
+    assert not torch.isfinite(dv[0, 0, :, 7]).any()
+    keep = torch.arange(260, device="cuda") != 150
+    assert torch.equal(dq[0, 0, keep], clean[0][0, 0, keep]) and torch.equal(dv[0, 0, :, 8:], clean[2][0, 0, :, 8:])
+    assert all(torch.equal(a[0, 1], b[0, 1]) for a, b in zip((dq, dk, dv), clean))
+
+
+@pytest.mark.gpu
+def test_fp16_gradients_captured():
+    """The fp16 backward pass, whose kernels overlap, captured and replayed with other values, sizes of
+    dout and lengths; the workspace's norms are those of the replay."""
+    B, H, Tq, Tk, d = 2, 3, 400, 300, 128
+    q, k, v, _ = make(B, H, H, Tq, Tk, d, torch.float16, "bhtd", None, seed=8)
+    gen = torch.Generator(device="cuda").manual_seed(4)
+    dout = torch.randn(q.shape, generator=gen, device="cuda").half()
+    lens = torch.tensor([300, 140], dtype=torch.int32, device="cuda")
+    cfg = da2.cross_config(B, H, Tq, Tk, d, dtype=torch.float16)
+    out, lse, first = run_both(cfg, q, k, v, dout, lens)
+    ws, wsb = da2.cross_attention_workspace(cfg, "cuda"), da2.cross_attention_workspace(cfg, "cuda", backward=True)
+    grads = [torch.empty_like(x) for x in first]
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        da2.cross_attention(cfg, q, k, v, out, ws, kv_len=lens, lse=lse)
+        da2.cross_attention_backward(cfg, dout, q, k, v, out, lse, *grads, wsb, kv_len=lens)
+    graph.replay()
+    assert all(torch.equal(a, b) for a, b in zip(first, grads))
+    v.mul_(16.0)
+    dout.mul_(64.0)
+    for n in ([0, 257], [128, 300]):
+        lens.copy_(torch.tensor(n, dtype=torch.int32))
+        for _ in range(3):
+            graph.replay()
+        check_grads(grads, fp16_wants(q, k, v, dout, n), "bhtd")
