@@ -38,6 +38,7 @@ struct CrossArgs {
   int q_tiles, k_tiles;            // 128-row tiles
   float *lse2, *delta;             // fp32 [B*H][128 q_tiles]: lse in the log2 domain, D
   float* part_kv;                  // fp32 [2 sms][2][d][128]: dK and dV of split sums
+  int32_t* first;                  // [B + 1]: key tiles with a valid key in front of each batch entry
   float *dnorm2, *vnorm2;          // fp16: [B*H][q_tiles][4] and [B*Hkv][k_tiles], largest squared row norms
 };
 

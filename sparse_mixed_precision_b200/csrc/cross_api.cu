@@ -62,7 +62,7 @@ FwdLayout fwd_layout(const da2_cross_config* c) {
 }
 
 struct BwdLayout {
-  size_t lse2, delta, part, dnorm2, vnorm2, total;
+  size_t lse2, delta, part, first, dnorm2, vnorm2, total;
 };
 BwdLayout bwd_layout(const da2_cross_config* c) {
   BwdLayout l;
@@ -70,7 +70,8 @@ BwdLayout bwd_layout(const da2_cross_config* c) {
   l.lse2 = kErrBytes;
   l.delta = l.lse2 + rows * 4;
   l.part = l.delta + rows * 4;
-  l.dnorm2 = l.part + (size_t)2 * kSms * 2 * c->d * 128 * 4;
+  l.first = l.part + (size_t)2 * kSms * 2 * c->d * 128 * 4;
+  l.dnorm2 = l.first + align256(((size_t)c->B + 1) * 4);
   const bool f16 = c->dtype == DA2_DTYPE_F16;
   l.vnorm2 = l.dnorm2 + (f16 ? align256(rows / 128 * 16) : 0);
   l.total = l.vnorm2 + (f16 ? align256((size_t)c->B * c->Hkv * (((size_t)c->Tk + 127) / 128) * 4) : 0);
@@ -225,6 +226,7 @@ da2_status da2_cross_attention_backward(const da2_cross_config* cfg, const da2_t
   g.lse2 = reinterpret_cast<float*>(base + l.lse2);
   g.delta = reinterpret_cast<float*>(base + l.delta);
   g.part_kv = reinterpret_cast<float*>(base + l.part);
+  g.first = reinterpret_cast<int32_t*>(base + l.first);
   g.dnorm2 = reinterpret_cast<float*>(base + l.dnorm2);
   g.vnorm2 = reinterpret_cast<float*>(base + l.vnorm2);
   g.v = in[2];

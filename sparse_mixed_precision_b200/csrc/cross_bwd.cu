@@ -201,6 +201,23 @@ __device__ __forceinline__ void mma_rows(uint32_t acc, uint32_t a, uint32_t b, u
   }
 }
 
+// Live key tiles in front of each batch entry, and their number. A full warp.
+__device__ __noinline__ void count_tiles(const CrossArgs& g, int lane) {
+  int before = 0;
+  for (int b0 = 0; b0 < g.B; b0 += 32) {
+    const int b = b0 + lane, n = b < g.B ? (valid_keys(g, b) + 127) >> 7 : 0;
+    int sum = n;                                         // of the lanes up to this one
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int x = __shfl_up_sync(0xffffffffu, sum, o);
+      if (lane >= o) sum += x;
+    }
+    if (b < g.B) g.first[b] = before + sum - n;
+    before += __shfl_sync(0xffffffffu, sum, 31);
+  }
+  if (lane == 0) g.first[g.B] = before;
+}
+
 template <typename T, int D>
 __global__ void __launch_bounds__(kThreads, 1)
 k_cross_dq(const __grid_constant__ CrossMaps maps, const __grid_constant__ CrossArgs g) {
@@ -298,6 +315,7 @@ k_cross_dq(const __grid_constant__ CrossMaps maps, const __grid_constant__ Cross
     const uint32_t sm0 = tc::smem_u32(sm) >> 4, stage0 = sm0 + (S::kStage0 >> 4);
     uint32_t step = 0, n_items = 0;
     bool dead = false;
+    if (role == 2 && blockIdx.x == 0) count_tiles(g, lane);      // the role that waits longest at first
     for (int i = blockIdx.x; i < items && !dead; i += gridDim.x) {
       const ItemDq w(g, i);
       for (int t = 0; t < w.nt && !dead; ++t, ++step) {
@@ -568,38 +586,38 @@ static_assert(sizeof(BarsDkv<64>) <= 512, "barrier area");
 
 constexpr uint32_t kKvS = 0, kKvP = 128, kKvDv = 256, kKvDk = 384;    // columns
 
-// The live groups and how the blocks share them.
+// The live groups, numbered by batch entry, key/value head and key tile, and how the blocks share them.
+// first[b] (left by k_cross_dq) counts the live key tiles in front of batch entry b, of one head.
 struct Share {
   long units;                 // of all live groups
   int n;                      // units per group
   int blocks;
   __device__ __forceinline__ Share(const CrossArgs& g) {
-    long live = 0;
-    for (int b = 0; b < g.B; ++b) live += (valid_keys(g, b) + 127) >> 7;
     n = g.group * g.q_tiles;
-    units = live * g.Hkv * n;
+    units = (long)g.first[g.B] * g.Hkv * n;
     blocks = g.sms;
   }
   __device__ __forceinline__ long begin(int c) const { return units * c / blocks; }
 };
-// Live group i: batch entry, key/value head, key tile.
+// Live group i: batch entry, key/value head, key tile. The entry by bisection, so that long batches of
+// short sequences do not walk the batch for every group.
 struct Group {
   int b, hkv, kt, len;
-  __device__ __forceinline__ Group(const CrossArgs& g, long i) {
-    for (b = 0;; ++b) {
-      len = valid_keys(g, b);
-      const int tiles = (len + 127) >> 7;
-      const long here = (long)tiles * g.Hkv;
-      if (i < here || b == g.B - 1) {
-        hkv = (int)(i / max(tiles, 1));
-        kt = (int)(i - (long)hkv * tiles);
-        return;
-      }
-      i -= here;
+  __device__ __forceinline__ Group(const CrossArgs& g, uint32_t i) {
+    const int t = i / (uint32_t)g.Hkv;
+    int lo = 0, hi = g.B;                                // first[lo] <= t < first[hi]
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (g.first[mid] <= t) lo = mid;
+      else hi = mid;
     }
+    b = lo;
+    const uint32_t tiles = g.first[lo + 1] - g.first[lo], rest = i - (uint32_t)g.first[lo] * g.Hkv;
+    hkv = rest / tiles;
+    kt = rest - hkv * tiles;
+    len = valid_keys(g, b);
   }
 };
-
 template <typename T, int D>
 __global__ void __launch_bounds__(kThreads, 1)
 k_cross_dkv(const __grid_constant__ CrossMaps maps, const __grid_constant__ CrossArgs g) {
@@ -871,9 +889,7 @@ __global__ void __launch_bounds__(128) k_cross_dkv_join(const __grid_constant__ 
   for (int k = 0; k < 32; ++k) acc[k] = 0.0f;
   if (kt < tiles) {
     const Share sh(g);
-    long gi = (long)hkv * tiles + kt;
-    for (int i = 0; i < b; ++i) gi += (long)((valid_keys(g, i) + 127) >> 7) * g.Hkv;
-    const long a = gi * sh.n, e = a + sh.n;
+    const long a = ((long)g.first[b] * g.Hkv + hkv * tiles + kt) * sh.n, e = a + sh.n;
     int c = (int)(a * sh.blocks / sh.units);             // a block at or next to the first
     while (c > 0 && sh.begin(c) > a) --c;
     while (sh.begin(c + 1) <= a) ++c;

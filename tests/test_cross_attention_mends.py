@@ -130,3 +130,46 @@ def test_fp16_gradients_captured():
         for _ in range(3):
             graph.replay()
         check_grads(grads, fp16_wants(q, k, v, dout, n), "bhtd")
+
+
+# ------------------------------------------------------------------ long batches
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+def test_many_short_sequences_with_lengths_of_their_own(dtype):
+    """Hundreds of batch entries, some without a key, some with several key tiles."""
+    B, H, Hkv, Tq, Tk, d = 333, 4, 2, 9, 150, 64
+    gen = torch.Generator().manual_seed(7)
+    lens = [int(n) for n in torch.randint(-40, Tk + 1, (B,), generator=gen).clamp(min=0)]
+    q, k, v, kv_len = make(B, H, Hkv, Tq, Tk, d, dtype, "bhtd", lens, seed=2)
+    dout = torch.randn(q.shape, generator=torch.Generator(device="cuda").manual_seed(1), device="cuda").to(dtype)
+    cfg = da2.cross_config(B, H, Tq, Tk, d, Hkv=Hkv, dtype=dtype)
+    _, _, grads = run_both(cfg, q, k, v, dout, kv_len)
+    check_grads(grads, gradients64(q, k, v, dout, lens, "bhtd", dtype), "bhtd")
+
+
+@pytest.mark.gpu
+def test_backward_time_grows_with_the_batch_and_not_its_square():
+    """Frames or windows folded into the batch: eight times the entries may take twice as long an entry,
+    not eight times."""
+    H, T, d = 8, 8, 64
+
+    def time_of(B):
+        x = torch.randn(B, H, T, d, device="cuda").to(torch.bfloat16)
+        lse = torch.zeros(B, H, T, device="cuda")
+        lens = torch.full((B,), T, dtype=torch.int32, device="cuda")
+        cfg = da2.cross_config(B, H, T, T, d)
+        ws = da2.cross_attention_workspace(cfg, "cuda", backward=True)
+        grads = [torch.empty_like(x) for _ in range(3)]
+        best = float("inf")
+        for _ in range(4):
+            t = [torch.cuda.Event(enable_timing=True) for _ in range(2)]
+            t[0].record()
+            da2.cross_attention_backward(cfg, x, x, x, x, x, lse, *grads, ws, kv_len=lens)
+            t[1].record()
+            t[1].synchronize()
+            best = min(best, t[0].elapsed_time(t[1]))
+        assert da2.cross_attention_get_error(ws) == 0
+        return best
+
+    short, long = time_of(2048), time_of(16384)
+    assert long <= 16 * short, (short, long)
