@@ -467,7 +467,8 @@ k_cross_forward(const __grid_constant__ CrossMaps maps, const __grid_constant__ 
         ++n_items[x];
         ++tiles;
         tc::fence_after_sync();
-        const float inv = 1.0f / lm.x;
+        // a part whose scores are all -inf has no sum: no weight in the join, so its zeros must not turn NaN
+        const float inv = g.splits > 1 && lm.x == 0.0f ? 0.0f : 1.0f / lm.x;
 #pragma unroll 1
         for (int c0 = 0; c0 < D; c0 += 32) {
           uint32_t v[32];
@@ -524,15 +525,20 @@ k_cross_forward(const __grid_constant__ CrossMaps maps, const __grid_constant__ 
 }
 
 // Joins the parts of split keys: out = sum_s 2^(lse_s - max) o_s / sum_s 2^(lse_s - max), one warp
-// per row.
+// per row. No part with weight: zero without a valid key, NaN where every valid score is -inf or NaN (as
+// one part alone has it).
 template <typename T, int D>
 __global__ void __launch_bounds__(128) k_cross_join(const __grid_constant__ CrossArgs g) {
   const size_t rows = (size_t)g.B * g.H * g.Tq;
   const size_t row = (size_t)blockIdx.x * 4 + (threadIdx.x >> 5);
   const int lane = threadIdx.x & 31;
   if (row >= rows) return;
-  float m = -INFINITY;
-  for (int s = 0; s < g.splits; ++s) m = fmaxf(m, g.part_lse[s * rows + row]);
+  float m = -INFINITY, none = 0.0f;                      // none: -inf, or NaN, without a part of weight
+  for (int s = 0; s < g.splits; ++s) {
+    const float l = g.part_lse[s * rows + row];
+    m = fmaxf(m, l);
+    none += l;
+  }
   float acc[D / 32] = {}, total = 0.0f;
   if (m != -INFINITY) {
     for (int s = 0; s < g.splits; ++s) {
@@ -543,14 +549,14 @@ __global__ void __launch_bounds__(128) k_cross_join(const __grid_constant__ Cros
       for (int e = 0; e < D / 32; ++e) acc[e] = fmaf(w, o[e], acc[e]);
     }
   }
-  const float inv = m == -INFINITY ? 0.0f : 1.0f / total;
   const size_t bh = row / g.Tq;
   const int t = (int)(row - bh * g.Tq), b = (int)(bh / g.H), h = (int)(bh - (size_t)b * g.H);
+  const float inv = m == -INFINITY ? (valid_keys(g, b) > 0 ? NAN : 0.0f) : 1.0f / total;
   uint32_t* out = reinterpret_cast<uint32_t*>(static_cast<T*>(g.out.data) + b * g.out.sb + h * g.out.sh +
                                               t * g.out.st + lane * (D / 32));
 #pragma unroll
   for (int e = 0; e < D / 64; ++e) out[e] = pack16<T>(acc[2 * e] * inv, acc[2 * e + 1] * inv);
-  if (g.lse && lane == 0) g.lse[row] = m == -INFINITY ? -INFINITY : (m + log2f(total)) * kLn2;
+  if (g.lse && lane == 0) g.lse[row] = m == -INFINITY ? none : (m + log2f(total)) * kLn2;
 }
 
 template <typename T, int D>

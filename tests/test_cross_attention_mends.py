@@ -4,7 +4,7 @@ import pytest
 import torch
 
 import sparse_mixed_precision_b200 as da2
-from tests.test_cross_attention import make
+from tests.test_cross_attention import check_out, formulas64, make
 from tests.test_cross_attention_backward import check_grads, gradients64, run_both
 
 
@@ -173,3 +173,45 @@ def test_backward_time_grows_with_the_batch_and_not_its_square():
 
     short, long = time_of(2048), time_of(16384)
     assert long <= 16 * short, (short, long)
+
+
+# ------------------------------------------------------------------ parts without weight
+@pytest.mark.gpu
+@pytest.mark.parametrize("Tq", [1, 300])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+def test_keys_of_infinitely_low_score(Tq, dtype):
+    """Keys whose score is -inf, as a channel used for masking gives them: no weight, also where they fill
+    a whole part of the split keys; with no other key the softmax has no value."""
+    H, Tk, d = 2, 4096, 64
+    q, k, v, _ = make(2, H, H, Tq, Tk, d, dtype, "bhtd", None, seed=4)
+    q[..., 0] = 1
+    k[0, 0, :, 0] = torch.where(torch.arange(Tk, device="cuda") < 3900, -float("inf"), 0.0)
+    k[0, 1, 100:, 0] = -float("inf")
+    k[1, 1, :, 0] = -float("inf")
+    cfg = da2.cross_config(2, H, Tq, Tk, d, dtype=dtype)
+    ws = da2.cross_attention_workspace(cfg, "cuda")
+    assert ws.numel() > 256                             # the keys are split
+    out, lse = torch.empty_like(q), torch.empty(2, H, Tq, device="cuda")
+    da2.cross_attention(cfg, q, k, v, out, ws, lse=lse)
+    for b, h in ((0, 0), (0, 1), (1, 0)):
+        at = (slice(b, b + 1), slice(h, h + 1))
+        keys = {(0, 0): slice(3900, None), (0, 1): slice(0, 100), (1, 0): slice(None)}[b, h]
+        check_out(out[at], lse[at], formulas64(q[at], k[at][:, :, keys], v[at][:, :, keys], None, "bhtd"), dtype, "bhtd")
+    assert torch.isnan(out[1, 1]).all() and (lse[1, 1] == -float("inf")).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("Tk", [64, 4096])
+def test_a_nan_query_has_a_nan_row(Tk):
+    """With one part and with several: the row and its lse are NaN, the other rows are as without it."""
+    q, k, v, _ = make(1, 2, 2, 3, Tk, 128, torch.bfloat16, "bhtd", None, seed=4)
+    cfg = da2.cross_config(1, 2, 3, Tk, 128)
+    ws = da2.cross_attention_workspace(cfg, "cuda")
+    assert (ws.numel() > 256) == (Tk == 4096)
+    out, clean, lse = torch.empty_like(q), torch.empty_like(q), torch.empty(1, 2, 3, device="cuda")
+    da2.cross_attention(cfg, q, k, v, clean, ws, lse=lse)
+    q[0, 1, 1, 5] = float("nan")
+    da2.cross_attention(cfg, q, k, v, out, ws, lse=lse)
+    assert torch.isnan(out[0, 1, 1]).all() and torch.isnan(lse[0, 1, 1])
+    out[0, 1, 1] = clean[0, 1, 1]
+    assert torch.equal(out, clean) and torch.isnan(lse).sum() == 1
