@@ -429,7 +429,7 @@ k_cross_forward(const __grid_constant__ CrossMaps maps, const __grid_constant__ 
     issue<T, D, 1>(g, sm, bars, items, gd, lane);
   } else if (warp < kMmaWarp) {
     // No wait ends this loop early: all 128 threads must meet at the named barrier. After an abort
-    // every wait returns at once and what is written is undefined.
+    // every wait ends soon and what is written is undefined.
     const int r = tid & 127;
     const bool lead = tid == kEpiWarp * 32;
     const uint32_t lane_base = tmem + ((uint32_t)((warp & 3) * 32) << 16);

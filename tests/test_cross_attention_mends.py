@@ -215,3 +215,28 @@ def test_a_nan_query_has_a_nan_row(Tk):
     assert torch.isnan(out[0, 1, 1]).all() and torch.isnan(lse[0, 1, 1])
     out[0, 1, 1] = clean[0, 1, 1]
     assert torch.equal(out, clean) and torch.isnan(lse).sum() == 1
+
+
+# ------------------------------------------------------------------ calls that are given up
+@pytest.mark.gpu
+def test_an_aborted_call_ends_soon_after_the_limit():
+    """The test hook withholds each kernel's first load and its waits run out. What a long call then takes
+    beyond a short one, whose waits are few, is about its arithmetic (35 ms here), not the number of its
+    waits times their suspension."""
+    def stalled(H, Tq, Tk):
+        x = torch.zeros(1, H, Tq, 128, dtype=torch.bfloat16, device="cuda")
+        k, lse = x[:, :, :Tk].contiguous(), torch.zeros(1, H, Tq, device="cuda")
+        grads = [torch.empty_like(t) for t in (x, k, k)]
+        cfg = da2.cross_config(1, H, Tq, Tk, 128, flags=da2.FLAG_TEST_STALL)
+        ws = da2.cross_attention_workspace(cfg, "cuda", backward=True)
+        t = [torch.cuda.Event(enable_timing=True) for _ in range(2)]
+        t[0].record()
+        da2.cross_attention_backward(cfg, x, x, k, k, x, lse, *grads, ws)
+        t[1].record()
+        t[1].synchronize()
+        assert da2.cross_attention_get_error(ws) == 1
+        return t[0].elapsed_time(t[1])
+
+    stalled(2, 4096, 4096)                              # loads the kernels
+    short, long = stalled(2, 4096, 4096), stalled(40, 131072, 4096)
+    assert long - short < 45, (short, long)
