@@ -312,7 +312,7 @@ typedef struct da2_norm_rope_config {
      n = x / sqrt(mean_c(x_c^2) + eps),  y = n * w,
      (y_a, y_b) -> (y_a cos - y_b sin, y_a sin + y_b cos) for channel pair i = (a, b)
    with cos, sin = row t (the token) and column i of the tables. wq, wk: fp32 [d], shared by
-   the heads; NULL means all ones. cos_t, sin_t: fp32, 16-byte aligned; not read when T_rot is
+   the heads, 16-byte aligned; NULL means all ones. cos_t, sin_t: fp32, 16-byte aligned; not read when T_rot is
    0. q_out may be q and k_out may be k (the same pointer and strides). k and k_out are not
    read when Hk is 0 and may be NULL. A row of zeros with eps 0 gives NaN, like the formula. */
 da2_status da2_qk_norm_rope(const da2_norm_rope_config* cfg, const da2_tensor* q, const da2_tensor* k,
@@ -325,7 +325,7 @@ da2_status da2_qk_norm_rope_workspace_size(const da2_norm_rope_config* cfg, size
 /* Gradients of da2_qk_norm_rope: dq_out, dk_out are the gradients of its outputs, q, k its
    inputs. With g = the gradient rotated back,
      dw = sum over rows of g * n,  dx = (g w - n mean_c(g w n)) / sqrt(mean_c(x^2) + eps).
-   dq may be dq_out or q, dk may be dk_out or k. dwq, dwk: fp32 [d], overwritten (dwk is not
+   dq may be dq_out or q, dk may be dk_out or k. dwq, dwk: fp32 [d], 4-byte aligned, overwritten (dwk is not
    written when Hk is 0); NULL skips them, and with both NULL ws is not needed. The sums run in a fixed order: equal inputs give equal bits. ws: 256-byte aligned. */
 da2_status da2_qk_norm_rope_backward(const da2_norm_rope_config* cfg, const da2_tensor* dq_out,
                                      const da2_tensor* dk_out, const da2_tensor* q, const da2_tensor* k,

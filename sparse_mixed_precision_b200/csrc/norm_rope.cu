@@ -96,7 +96,8 @@ __device__ __forceinline__ void store_row(T* row, int c, const float* x) {
   __stcs(reinterpret_cast<uint4*>(row + 8 * c), make_uint4(u[0], u[1], u[2], u[3]));
   __stcs(reinterpret_cast<uint4*>(row + D / 2 + 8 * c), make_uint4(u[4], u[5], u[6], u[7]));
 }
-// A thread's 16 weights, laid out like its elements.
+// A thread's 16 weights, laid out like its elements (16-byte aligned: a branch for other addresses took
+// 5 % of the forward pass's time).
 template <int D>
 __device__ __forceinline__ void load_weight(const float* w, int c, float* x) {
 #pragma unroll
@@ -413,7 +414,8 @@ da2_status da2_qk_norm_rope_backward(const da2_norm_rope_config* cfg, const da2_
   float* dw[2] = {dwq, dwk};
   if (dwq || dwk) {
     if (!ws) return DA2_ERR_INVALID_ARG;
-    if ((reinterpret_cast<uintptr_t>(ws) & 255u) != 0 || !aligned16(dwq) || !aligned16(dwk))
+    if ((reinterpret_cast<uintptr_t>(ws) & 255u) != 0 ||
+        ((reinterpret_cast<uintptr_t>(dwq) | reinterpret_cast<uintptr_t>(dwk)) & 3u) != 0)
       return DA2_ERR_ALIGNMENT;
     if (ws_bytes < dw_bytes(cfg)) return DA2_ERR_WORKSPACE;
   }
