@@ -26,7 +26,6 @@ struct CrossArgs {
   long long wait_clocks;           // limit of every bounded device wait
   int stall;                       // test hook: the first load is withheld
   int sms;                         // processors of the device
-  int heads_first;                 // neighbouring blocks take the heads of the same query rows
   // forward
   da2_tensor out;
   float* lse;                      // null: not wanted

@@ -131,10 +131,6 @@ da2_status common_args(const da2_cross_config* c, const da2_tensor* q, const da2
   g->err = static_cast<uint32_t*>(ws);
   g->stall = (c->flags & DA2_FLAG_TEST_STALL) != 0;
   // about 2 s, longer than anything here waits; the test hook shortens it to about 50 ms
-  // Token-major queries: the rows of one token's heads are neighbours, so heads go first as long as
-  // the keys and values of one batch entry stay in L2 (126 MB, shared with the query stream) anyway.
-  g->heads_first = c->H > 1 && c->Tq > 1 && in[0].sh < in[0].st &&
-                   (long)c->Hkv * c->Tk * c->d * 4 <= (long)40 << 20;
   g->wait_clocks = g->stall ? 100000000ll : 4000000000ll;
   return DA2_OK;
 }

@@ -168,17 +168,10 @@ struct ItemDq {
   // not inline: its divisions in each of the kernel's roles would crowd the instruction cache
   static __device__ __noinline__ void decode(const CrossArgs& g, uint32_t u, int* v) {
     int b, h, qt;
-    if (g.heads_first) {
-      const uint32_t bp = u / g.H;
-      h = u - bp * g.H;
-      b = bp / g.q_tiles;
-      qt = bp - b * g.q_tiles;
-    } else {
-      const uint32_t bh = u / g.q_tiles;
-      qt = u - bh * g.q_tiles;
-      b = bh / g.H;
-      h = bh - b * g.H;
-    }
+    const uint32_t bh = u / g.q_tiles;
+    qt = u - bh * g.q_tiles;
+    b = bh / g.H;
+    h = bh - b * g.H;
     const int len = valid_keys(g, b);
     v[0] = b, v[1] = h, v[2] = qt, v[3] = (len + 127) >> 7, v[4] = len;
   }
