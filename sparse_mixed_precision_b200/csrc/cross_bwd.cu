@@ -224,6 +224,7 @@ k_cross_dq(const __grid_constant__ CrossMaps maps, const __grid_constant__ Cross
   const Guard gd{g.err, &bars->abort, g.wait_clocks};
   if (tc::smem_u32(sm) & 1023u) {        // the swizzle needs the alignment that the declaration asks for
     if (tid == 0) set_error(g.err, kErrBadIndex);
+    if (blockIdx.x == 0 && warp == 0) count_tiles(g, lane);      // k_cross_dkv indexes by it
     return;
   }
 
@@ -926,7 +927,8 @@ cudaError_t launch(const CrossArgs& g, const CrossMaps& m, cudaStream_t st) {
   early.val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = &early;
   cfg.numAttrs = Scale<T>::kBf16 ? 0 : 1;
-  e = cudaLaunchKernelEx(&cfg, k_cross_dq<T, D>, m, g);
+  cudaLaunchKernelEx(&cfg, k_cross_dq<T, D>, m, g);
+  e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   k_cross_dkv<T, D><<<g.sms, kThreads, SmemDkv<D>::kBytes, st>>>(m, g);
   e = cudaGetLastError();
