@@ -16,6 +16,10 @@ inline size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
 
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
+// Longest token axis of the operators around the self-attention: lengths are rounded up to whole tiles
+// (of 256 at most) in 32 bits.
+constexpr int kMaxTokens = 0x7fffffff - 255;
+
 // An NVTX range around one library call (visible in a profiler's timeline; no cost without
 // an attached tool).
 struct NvtxRange {

@@ -19,6 +19,7 @@ da2_status check_cross_config(const da2_cross_config* c) {
   if (c->dtype != DA2_DTYPE_BF16 && c->dtype != DA2_DTYPE_F16) return DA2_ERR_INVALID_ARG;
   if (c->flags & ~DA2_FLAG_TEST_STALL) return DA2_ERR_INVALID_ARG;
   if (c->d != 64 && c->d != 128) return DA2_ERR_UNSUPPORTED;
+  if (c->Tq > kMaxTokens || c->Tk > kMaxTokens) return DA2_ERR_UNSUPPORTED;
   // work items and rows are counted in 32 bits, with room for 64 parts of the keys
   const long heads = (long)c->B * c->H;
   if (heads > (1L << 24)) return DA2_ERR_UNSUPPORTED;

@@ -314,6 +314,7 @@ da2_status check_norm_config(const da2_norm_rope_config* c) {
   if (c->dtype != DA2_DTYPE_BF16 && c->dtype != DA2_DTYPE_F16) return DA2_ERR_INVALID_ARG;
   if (c->flags & ~(DA2_ROPE_HALVES | DA2_ROPE_BATCHED)) return DA2_ERR_INVALID_ARG;
   if (c->d != 64 && c->d != 128) return DA2_ERR_UNSUPPORTED;
+  if (c->T > kMaxTokens) return DA2_ERR_UNSUPPORTED;
   // the grid holds at most one block per token block, head and batch entry
   if (((long)c->T + 31) / 32 * c->B > (1L << 30) / ((long)c->Hq + c->Hk)) return DA2_ERR_UNSUPPORTED;
   return DA2_OK;
