@@ -282,7 +282,15 @@ const char* da2_status_string(da2_status status);
  * (DA2_ERR_INVALID_ARG otherwise: rows would overlap); the stride of an axis of length one is
  * not read. Outputs must not overlap each other or, but
  * where a call says otherwise, an input. d is 64 or 128 and the element type bf16 or fp16.
- * Every sum, norm and softmax statistic is fp32; each output is rounded once.
+ * Every sum, norm and softmax statistic is fp32; each output is rounded once. The attention's tensor
+ * cores take 16-bit operands: p (forward) and p and dS (backward) are rounded to the element type in
+ * between, once each, and D is formed from the rounded out. Against 64 bits the attention's results are
+ * off by 1.2 to 1.5 times what the rounding of the outputs alone makes (relative L2 0.0020 to 0.0024 instead
+ * of 0.0017 in bf16, 0.0003 instead of 0.0002 in fp16).
+ * da2_prepare takes bf16, and the self-attention has no backward pass: in a block of this library the
+ * bf16 forms of the norm feed it, and gradients reach the norms of the attention to the encoder's states;
+ * fp16 and the rotation's gradient are for a caller's own self-attention.
+ * At most 2^31 - 256 tokens an axis (DA2_ERR_UNSUPPORTED otherwise).
  * The calls are asynchronous on `stream`, allocate nothing, keep nothing between calls and
  * can be captured into a CUDA graph; two calls that may overlap need workspaces of their own. */
 typedef struct da2_tensor {
@@ -308,7 +316,8 @@ typedef struct da2_norm_rope_config {
   int flags;            /* DA2_ROPE_* bits */
 } da2_norm_rope_config;
 
-/* RMS norm of each head of q and k and the position rotation, in one pass:
+/* RMS norm of each head of q and k (over its own d channels, not over all heads' together) and the
+   position rotation, in one pass:
      n = x / sqrt(mean_c(x_c^2) + eps),  y = n * w,
      (y_a, y_b) -> (y_a cos - y_b sin, y_a sin + y_b cos) for channel pair i = (a, b)
    with cos, sin = row t (the token) and column i of the tables. wq, wk: fp32 [d], shared by
@@ -353,7 +362,9 @@ da2_status da2_cross_attention_backward_workspace_size(const da2_cross_config* c
      lse = ln sum exp(s)  (fp32 [B][H][Tq]; NULL: not written).
    kv_len: device int32 [B], each taken into 0 .. Tk; NULL: Tk for every batch entry. Keys and
    values behind the length do not reach the result, whatever they hold. A batch entry of length
-   0 has out = 0 and lse = -inf. Few query rows are split over their keys, the parts joined in a
+   0 has out = 0 and lse = -inf. Scores |s| up to 5e7: beyond, the fp32 exponent's own rounding takes p
+   out of the element type's range. Within the length infinities and NaN count as the formula has it: a
+   key of score -inf has no weight, and a row without any weight is NaN. Few query rows are split over their keys, the parts joined in a
    fixed order: equal inputs give equal bits.
    ws: 256-byte aligned; its first 256 bytes are the error area, to be zeroed once after the
    workspace is allocated. A bounded device wait that runs out sets a bit there
@@ -367,7 +378,8 @@ da2_status da2_cross_attention(const da2_cross_config* cfg, const da2_tensor* q,
      dq = sm_scale dS k,  dk = sm_scale dS^T q,  dv = p^T dout  (dk, dv summed over the query
    heads that share a key/value head).
    Every row of dq, dk and dv is written: zero for keys behind the length and for batch entries of
-   length 0. The sums run in a fixed order. ws as above, of the backward pass's own size. */
+   length 0. p comes from lse, whose rounding makes it relatively off by up to |lse| 2^-23. In fp16 dS
+   carries powers of two from the norms of dout and v, so that any dout whose gradients fit fp16 will do. The sums run in a fixed order. ws as above, of the backward pass's own size. */
 da2_status da2_cross_attention_backward(const da2_cross_config* cfg, const da2_tensor* dout,
                                         const da2_tensor* q, const da2_tensor* k, const da2_tensor* v,
                                         const da2_tensor* out, const float* lse, const int32_t* kv_len,

@@ -32,8 +32,12 @@ long q_pairs(const da2_cross_config* c) { return (c->Tq + 255) / 256; }
 
 // Parts that the keys of one query tile are split into, so that few query rows still fill the
 // processors. In units of 128 keys' time: a wave of items costs its keys plus about two for filling the
-// pipeline and the epilogue, and joining costs about four, plus the parts' traffic (40 heads, one query,
-// 512 keys: 16.4 us unsplit, 18.4 in two parts).
+// pipeline and the epilogue, and joining costs about four, plus the parts' traffic. Measured with the rule's
+// parts and others (single calls, us): 40 items on 512 keys 19.5 whole, 23.6 in two parts (rule: whole); 48
+// on 4096 keys 87 whole, 62 in two, 54 in three (rule); 80 on 4096 keys 66.6 whole, 60 to 62 in three
+// (rule), 62.5 in eight; 120 and 147 on 4096 keys 71 and 73 whole (rule), 81 in two. From 148 items on nothing is
+// split: right at 290 (128 whole, 138 in two), not just above 148 (150 items 123 whole, 105 in two, 93 in
+// eight).
 int choose_splits(const da2_cross_config* c) {
   const long units = (long)c->B * c->H * q_pairs(c), steps = ((long)c->Tk + 127) / 128;
   if (units >= kSms || steps < 2) return 1;

@@ -7,8 +7,9 @@
 // tile and walks the keys; k_cross_dkv holds one key tile and walks the queries. Each recomputes
 // S and dP, which makes seven products of five; accumulating dq over key tiles in memory instead
 // would move 8 bytes per element and key tile, more time than the two products.
-// Measured (40 heads, d = 128, bf16, 32760 queries, 512 keys): 1270 us for both, 680 TFLOP/s of the five
-// products that the gradients cannot do without, 950 of the seven. Bound now by each step's chain of
+// Measured (40 heads, d = 128, bf16, 32760 queries, 512 keys): 1230 us for both in 20 calls at 1965 MHz, 700
+// TFLOP/s of the five products that the gradients cannot do without, 980 of the seven; 1400 us in a second
+// and a half of calls, where the power cap leaves about 1570 MHz. Bound now by each step's chain of
 // reading S and dP, the exponentials, and handing P and dS back to the tensor cores, and in dq by the
 // change of query tiles (about 5000 cycles against 2000 a step of 1540 of MMA time).
 //

@@ -23,9 +23,11 @@
 // takes 48 cycles per MMA where 128 take 64, 1242 cycles for the pair. In the last step only the 16-key
 // groups that hold a valid key are multiplied.
 //
-// Measured, 40 heads, d = 128, bf16, 32760 queries: 512 keys 370 us = 930 TFLOP/s, 2048 keys 1300 us =
-// 1060 TFLOP/s, 64 keys 143 us (the bytes alone take 102). What bounds it now: instruction fetch and
-// hand-offs, about 2000 cycles a step against 1242. Dropped, each slower on the 512-key case: one S
+// Measured, 40 heads, d = 128, bf16, 32760 queries, in 20 calls at 1965 MHz and in a second and a half of
+// calls, where the power cap leaves about 1640 MHz: 512 keys 376 us = 914 TFLOP/s and 427 us = 805, 2048
+// keys 1329 us = 1034 TFLOP/s and 1498 us = 917, 64 keys 147 and 152 us (the bytes alone take 102). What
+// bounds it now: instruction fetch and hand-offs, about 2000 cycles a step against 1242. Dropped, each
+// slower on the 512-key case: one S
 // buffer of 128 columns per tile (435 us; 510 with the row in registers), one issuing warp, MMAs issued
 // from inside one lane's branch (75 cycles each to issue instead of 16 to 32), polling waits, a degree-4
 // polynomial for an eighth to a half of the exponentials (no gain: they are not the bound).
@@ -277,7 +279,6 @@ k_cross_forward(const __grid_constant__ CrossMaps maps, const __grid_constant__ 
   tc::fence_after_sync();
   constexpr uint32_t tmem = 0;             // all 512 columns are this block's: the base is column 0
 
-  // registers: 2 x 152 + 2 x 104 = 4 x 128, the launch's
   if (warp < kEpiWarp) {
     const int x = warp >> 2, r = tid & 127;
     const uint32_t lane_base = tmem + ((uint32_t)((warp & 3) * 32) << 16);

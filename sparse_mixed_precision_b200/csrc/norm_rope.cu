@@ -10,9 +10,11 @@
 // and out together; each thread therefore keeps its 8 pairs' cos and sin in registers and
 // walks over the heads of its token. A thread owns two 16-byte chunks of the row, d/2 apart, so
 // that both members of a pair are its own in either pairing; d/16 threads share a row.
-// Measured (40 heads, d = 128, bf16; copy bandwidth 6552 GB/s): forward, 32760 tokens token-major
-// 238 us = 5700 GB/s, 75600 tokens head-major 531 us = 5900 GB/s; backward, 32760 tokens 406 us =
-// 5000 GB/s, bound by its arithmetic (about 250 instructions per 16 elements) beside the memory.
+// Measured in a sequence of calls (40 heads, d = 128, bf16; copy bandwidth 6552 GB/s): forward, 32760 tokens
+// token-major 240 us = 5650 GB/s, 75600 tokens head-major 535 us = 5850 GB/s; backward, 32760 tokens 409
+// us = 4970 GB/s. The backward pass waits for memory: 122 registers leave two blocks per processor (24 % of
+// the warps), each thread has the two rows of one head in flight, and 4.6 of 5.6 stalled cycles per
+// instruction are on loads; its arithmetic would take about 150 us.
 #include <cmath>
 
 #include <cuda_fp16.h>
@@ -204,9 +206,9 @@ __global__ void __launch_bounds__(kThreads) k_norm_rope(NormRopeArgs g) {
 }
 
 // The backward pass walks a fixed number of blocks per side over the items, so that each block
-// sums its rows' share of dw in registers and writes one partial row. One head at
-// a time: the 480p layer takes 419 us so, 532 with two in flight, whose registers leave one block per
-// processor, and 439 with four.
+// sums its rows' share of dw in registers and writes one partial row. One head at a time: with two
+// in flight, whose registers leave one block per processor, the 480p layer took 532 us where it took 419,
+// with four 439.
 template <typename T, int D, bool HALVES>
 __global__ void __launch_bounds__(kThreads) k_norm_rope_back(NormRopeArgs g) {
   constexpr int G = D / 16;
